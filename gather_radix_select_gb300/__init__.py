@@ -1,6 +1,6 @@
 """gather_radix_select_gb300 -- batched row-wise top-k and flat row gather on GB300.
 
-Python face of the C ABI in ``include/sel.h`` (libsel.so, built in-tree for
+Python face of the C ABI in ``include/sel.h`` and ``include/sel/cache.h`` (libsel.so, built in-tree for
 sm_103a by ``gather_radix_select_gb300.build``).  PyTorch supplies device
 memory and the current CUDA stream; every step of the computation runs in
 the library's kernels.  There is no CPU fallback: without the built library
@@ -19,8 +19,10 @@ import torch
 
 from . import _native
 from ._native import SelError, SEL_MAX_K
+from .cache import cache_attention, cache_gather, cache_write
 
-__all__ = ["topk", "gather_rows", "gather_rows_pair", "topk_gather", "block_topk_gather", "stride_requirement", "max_cols", "workspace_size", "kernel_name",
+__all__ = ["topk", "gather_rows", "gather_rows_pair", "topk_gather", "block_topk_gather", "cache_write", "cache_gather",
+           "cache_attention", "stride_requirement", "max_cols", "workspace_size", "kernel_name",
            "set_tuning", "get_tuning", "SelError",
            "SEL_MAX_K", "library_path"]
 

@@ -44,7 +44,8 @@ def sources() -> list[str]:
 
 def _deps() -> list[str]:
     files = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if not f.startswith(".")]
-    files.append(os.path.join(ROOT, "include", "sel.h"))
+    for where, _, names in os.walk(os.path.join(ROOT, "include")):
+        files += [os.path.join(where, f) for f in names if f.endswith(".h")]
     return files
 
 
