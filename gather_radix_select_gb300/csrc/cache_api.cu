@@ -9,6 +9,7 @@
 namespace {
 
 constexpr int64_t kIntMax = 0x7fffffffLL;
+constexpr int64_t kMaxPositions = kIntMax - 255;  // of a sequence: a tile's last position is an int too
 constexpr float kLog2e = 1.4426950408889634f;
 
 bool aligned(const void *p, int64_t a) { return reinterpret_cast<uintptr_t>(p) % static_cast<uintptr_t>(a) == 0; }
@@ -146,7 +147,7 @@ size_t sel_cache_attention_workspace_size(int64_t rows, int64_t h, int64_t d, in
         max_pages < 0 || page_size < 1 || n < 0)
         return 0;
     const int64_t cap = product(max_pages, page_size);
-    if (cap < 0 || cap > kIntMax || n > kIntMax || product(rows, h) < 0 || rows * h > kIntMax) return 0;
+    if (cap < 0 || cap > kMaxPositions || n > kMaxPositions || product(rows, h) < 0 || rows * h > kIntMax) return 0;
     return sel::cache_attention_workspace(rows, h, d, dv, b, idx_given ? n : cap, idx_given != 0);
 }
 
@@ -165,14 +166,14 @@ int sel_cache_attention(const void *q, int64_t rows, int64_t h, int64_t q_row_st
         if (idx_dtype != SEL_I32 && idx_dtype != SEL_I64) return SEL_EINVAL;
         if (n < 0 || (rows > 1 && idx_row_stride < n)) return SEL_EINVAL;
         if (!aligned(idx, idx_dtype == SEL_I64 ? 8 : 4)) return SEL_EALIGN;
-        if (n > kIntMax) return SEL_EUNSUPPORTED;
+        if (n > kMaxPositions) return SEL_EUNSUPPORTED;
     }
     if (rows == 0) return SEL_OK;
     if (!q || !out) return SEL_EINVAL;
     if (q_row_stride < 0 || q_head_stride < 0) return SEL_EINVAL;
     if (dv % 8 != 0 || !aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(end, 4)) return SEL_EALIGN;
     if ((rows > 1 && q_row_stride % 8 != 0) || (h > 1 && q_head_stride % 8 != 0)) return SEL_EALIGN;
-    if (cache->d > SEL_CACHE_ATTN_MAX_D || product(max_pages, cache->page_size) > kIntMax) return SEL_EUNSUPPORTED;
+    if (cache->d > SEL_CACHE_ATTN_MAX_D || product(max_pages, cache->page_size) > kMaxPositions) return SEL_EUNSUPPORTED;
     if (product(rows, h) < 0 || rows * h > kIntMax) return SEL_EUNSUPPORTED;
     const size_t need = sel_cache_attention_workspace_size(rows, h, cache->d, dv, b, max_pages, cache->page_size,
                                                            idx != nullptr, idx ? n : 0);

@@ -1,122 +1,848 @@
-// cache_attention.cu -- attention of new tokens over a paged cache: the plain kernel.
+// cache_attention.cu -- attention of new tokens over a paged cache, on the fifth-generation tensor cores.
 //
-// One CTA per (row, head).  Tiles of kTile positions: each thread forms the score of one key row, the
-// tile's largest score joins the running maximum, the running sum and accumulators are rescaled by
-// exp2(old - new), and each thread then adds its value columns' share.  Everything is in fp32.
+// For the columns n = (row, head) of one CTA and a tile of 128 positions with rows K:
+//     S^T = K Q^T            [128 positions x 64 columns]
+//     P^T = exp2(S^T * scale - ref)
+//     O^T += K[:, :dv]^T P^T [dv x 64 columns]
+// Positions are the M dimension of the first product and heads its N dimension, so a single token with
+// few heads wastes no part of the 128-row instruction, a thread of the softmax holds one position, and
+// the value is the key tile itself, read with the other dimension contiguous: each cache row is staged
+// once and used for both products.
+//
+// The sum of exponentials needs no maximum, only a reference that keeps exp2 in range.  `ref` is the
+// column's largest score when it was last set; while no score exceeds it by more than 2^8 the tile is
+// taken with one vote.  Else the columns' maxima are formed across the positions and the sums and
+// accumulators are rescaled.  Sums are kept per thread (its positions) and joined at the end.
+//
+// A CTA is 20 warps: 8 of softmax (two groups of 4: 32 columns each), 4 of which one issues the products,
+// 8 that stage rows, chunks of 128 columns by 128 positions in a ring.  A chunk is released when its part
+// of the second product is done, so the next tile's rows arrive while the rest of the product runs.
+//
+// Few rows over long contexts are split into parts of the positions, whose sums and accumulators a
+// second kernel joins in a fixed order.
+#include <cstddef>
 #include <cstdint>
 
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
 #include "cache_internal.h"
+#include "tcgen05.cuh"
 
 namespace sel {
 namespace {
 
-constexpr int kTile = 256;
-constexpr int kMaxD = 512;
+constexpr int kCols = 64;                  // (row, head) columns of a CTA
+constexpr int kTile = 128;                 // positions of a tile
+constexpr int kChunkBytes = kTile * 256;   // 128 positions x 128 columns of bf16
+constexpr int kHalfBytes = kChunkBytes / 2;  // 64 columns: one 128-byte line a position
+constexpr int kQHalf = kCols * 128;        // 64 query columns x 64 elements
+constexpr int kPBytes = kTile * 128;       // P^T: 128 positions x 64 columns
+constexpr int kSoftWarps = 8, kLoadWarps = 8;
+constexpr int kMmaWarp = kSoftWarps;           // its group of 4 warps holds one that works
+constexpr int kLoadWarp0 = kSoftWarps + 4;
+constexpr int kThreads = (kLoadWarp0 + kLoadWarps) * 32;
+// Registers a thread after the roles part, out of the 640 x 96 of the launch:
+// 256 x 144 + 128 x 40 + 256 x 72 = 60416 <= 61440.
+constexpr int kSoftRegs = 144, kMmaRegs = 40, kLoadRegs = 72;
+constexpr int kMaxRing = 5;
+constexpr int kValidSlots = 16;            // tiles whose validity bits are kept (more than the ring holds)
+constexpr int kMaxSplit = 64;
+constexpr float kRefSlack = 8.0f;          // log2: how far a score may exceed its column's reference
+constexpr long long kWaitCycles = 4000000000LL;  // about 2 s
+constexpr uint32_t kSuspend = 1000;
+constexpr int32_t kTimeout = 5;            // SEL_ETIMEOUT
 
-__device__ __forceinline__ float elem(const CacheRef &c, int64_t row, int64_t srow, int e)
+template <int C>
+struct Cfg {
+    static constexpr int ring = C <= 1 ? 5 : 4;          // chunks staged
+    static constexpr int pbufs = C <= 2 ? 2 : 1;
+    static constexpr bool ahead = ring >= 2 * C;         // the next tile's scores before this one's values
+    static constexpr int q_off = ring * kChunkBytes;
+    static constexpr int p_off = q_off + C * 2 * kQHalf;
+    static constexpr int misc_off = p_off + pbufs * kPBytes;
+};
+
+struct Misc {
+    uint64_t full[kMaxRing], empty[kMaxRing], s_full[2], s_empty[2], p_full[2], pv_done[2], q_full;
+    uint32_t tmem;
+    int abort;
+    int last;                 // selected positions: entries up to the last valid one
+    int range[2];             // smallest and largest end of the CTA's rows
+    alignas(16) int end[kCols];  // exclusive end of each column's row, 0 for unused columns
+    alignas(16) float ref[kCols];  // read 16 bytes at a time
+    alignas(16) float factor[kCols];
+    alignas(16) float inv[kCols];
+    alignas(16) int wmax[2][4][32];
+    alignas(16) float lsum[4][kCols];
+    alignas(16) uint32_t valid[kValidSlots][4];  // bit k of word w: position 32 w + k of the tile has a cache row
+};
+
+static_assert(offsetof(Misc, ref) % 16 == 0 && offsetof(Misc, factor) % 16 == 0 && offsetof(Misc, valid) % 16 == 0, "");
+
+struct Plan {
+    int rows_per_tile;   // T
+    int heads_per_tile;  // heads of a head block
+    int head_blocks;
+    int64_t tiles_per_seq;
+    int64_t items;       // CTAs of one part
+    int parts;
+};
+
+struct Kargs {
+    CacheAttnArgs a;
+    Plan p;
+    float *part_o;   // [rows * h][parts][dv]
+    float2 *part_ml; // [rows * h][parts]: reference (log2), sum
+};
+
+struct Waiter {
+    volatile int *abort;
+    int32_t *err;
+    // Waits until the phase of `parity` has completed.  After about 2 s without that, or once another
+    // thread gave up, it returns all the same: every loop has a fixed count, so the CTA ends, with
+    // SEL_ETIMEOUT in err_flag.
+    __device__ __forceinline__ void operator()(uint64_t *bar, int parity) const
+    {
+        if (mbar_try_wait(bar, static_cast<uint32_t>(parity), kSuspend)) return;
+        slow(bar, parity);
+    }
+    __device__ __forceinline__ void slow(uint64_t *bar, int parity) const
+    {
+        const long long t0 = clock64();
+        while (!mbar_try_wait(bar, static_cast<uint32_t>(parity), kSuspend)) {
+            if (*abort) return;
+            if (clock64() - t0 > kWaitCycles) {
+                *abort = 1;
+                if (err) atomicCAS(err, 0, kTimeout);
+                return;
+            }
+        }
+    }
+};
+
+// Order-preserving int of a float (for the integer warp maximum), and back.
+__device__ __forceinline__ int order_of(float x)
 {
-    if (!c.scales)
-        return __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t *>(c.data)[row + e]) << 16);
-    const __nv_fp8_storage_t code = static_cast<const uint8_t *>(c.data)[row + e];
-    const float v = __half2float(__half(__nv_cvt_fp8_to_halfraw(code, __NV_E4M3))) * c.scales[srow + e / kCacheGroup];
-    return __bfloat162float(__float2bfloat16_rn(v));
+    const int i = __float_as_int(x);
+    return i ^ ((i >> 31) & 0x7fffffff);
+}
+__device__ __forceinline__ float float_of(int i) { return __int_as_float(i ^ ((i >> 31) & 0x7fffffff)); }
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
+{
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-__global__ void __launch_bounds__(kTile) attention_plain_kernel(const CacheAttnArgs a)
+// What a CTA works on.
+struct Work {
+    int64_t row0, seq;
+    int rows, head0, heads;  // its rows and heads
+    int part;
+    __device__ __forceinline__ int cols() const { return rows * heads; }
+};
+
+__device__ __forceinline__ Work work_of(const Kargs &k)
 {
-    __shared__ float s_q[kMaxD];
-    __shared__ float s_p[kTile];
-    __shared__ int64_t s_row[kTile], s_scale[kTile];
-    __shared__ float s_red[kTile / 32];
-    const int t = threadIdx.x;
-    const int64_t row = blockIdx.x;
-    const int head = blockIdx.y;
-    const int64_t seq = row / a.t.rows_per_seq;
-    const uint16_t *q = a.q + row * a.q_row_stride + head * a.q_head_stride;
-    for (int e = t; e < a.d; e += kTile) s_q[e] = __uint_as_float(static_cast<uint32_t>(q[e]) << 16);
-    const int64_t cap = a.t.max_pages * a.c.page_size;
-    int64_t end = a.end ? a.end[row] : cap;
-    end = end < 0 ? 0 : (end > cap ? cap : end);
-    const int64_t keys = a.idx ? a.n : end;
-    float m = -INFINITY, l = 0.0f, acc[2] = {0.0f, 0.0f};
-    for (int64_t k0 = 0; k0 < keys; k0 += kTile) {
-        __syncthreads();
-        int64_t pos = -1;
-        if (k0 + t < keys) {
-            pos = k0 + t;
-            if (a.idx) {
-                const int64_t off = row * a.idx_row_stride + k0 + t;
-                pos = a.idx_i64 ? static_cast<const int64_t *>(a.idx)[off]
+    Work w;
+    // the last rows first: in a causal chunk they have the most positions
+    const int64_t item = k.p.items - 1 - blockIdx.x;
+    w.part = blockIdx.y;
+    const int64_t tile = item / k.p.head_blocks;
+    const int hb = static_cast<int>(item - tile * k.p.head_blocks);
+    w.seq = tile / k.p.tiles_per_seq;
+    const int64_t in_seq = (tile - w.seq * k.p.tiles_per_seq) * k.p.rows_per_tile;
+    w.row0 = w.seq * k.a.t.rows_per_seq + in_seq;
+    const int64_t left = k.a.t.rows_per_seq - in_seq;
+    w.rows = static_cast<int>(left < k.p.rows_per_tile ? left : k.p.rows_per_tile);
+    w.head0 = hb * k.p.heads_per_tile;
+    w.heads = min(k.p.heads_per_tile, k.a.h - w.head0);
+    return w;
+}
+
+// The position in entry j of a row's list, or -1 when it stands for none.
+__device__ __forceinline__ int64_t listed(const CacheAttnArgs &a, int64_t row, int64_t j, int64_t end, int64_t cap)
+{
+    const int64_t off = row * a.idx_row_stride + j;
+    const int64_t p = a.idx_i64 ? static_cast<const int64_t *>(a.idx)[off]
                                 : static_cast<int64_t>(static_cast<const int32_t *>(a.idx)[off]);
-                const bool past = pos >= cap;
-                if (past && a.err_flag) atomicCAS(a.err_flag, 0, kCacheInval);
-                if (pos >= end) pos = -1;
-            }
-        }
-        int64_t page = 0, place = 0;
-        float z = -INFINITY;
-        int64_t at = -1, sat = 0;
-        if (pos >= 0) {
-            if (find_row(a.c, a.t, seq, pos, page, place)) {
-                at = page * a.c.page_stride + place * a.c.row_stride;
-                sat = page * a.c.scale_page_stride + place * a.c.scale_row_stride;
-                float dot = 0.0f;
-                for (int e = 0; e < a.d; ++e) dot += s_q[e] * elem(a.c, at, sat, e);
-                z = dot * a.scale_log2;
-            } else if (a.err_flag) {
-                atomicCAS(a.err_flag, 0, kCacheInval);
-            }
-        }
-        s_row[t] = at;
-        s_scale[t] = sat;
-        float zm = z;
-        for (int o = 16; o > 0; o >>= 1) zm = fmaxf(zm, __shfl_xor_sync(0xffffffffu, zm, o));
-        if ((t & 31) == 0) s_red[t >> 5] = zm;
-        __syncthreads();
-        float m_new = m;
-        for (int w = 0; w < kTile / 32; ++w) m_new = fmaxf(m_new, s_red[w]);
-        const float base = m_new == -INFINITY ? 0.0f : m_new;
-        const float p = at < 0 ? 0.0f : exp2f(z - base);
-        const float f = exp2f(m - base);
-        s_p[t] = __bfloat162float(__float2bfloat16_rn(p));
-        float ps = p;
-        for (int o = 16; o > 0; o >>= 1) ps += __shfl_xor_sync(0xffffffffu, ps, o);
-        __syncthreads();
-        if ((t & 31) == 0) s_red[t >> 5] = ps;
-        __syncthreads();
-        float sum = 0.0f;
-        for (int w = 0; w < kTile / 32; ++w) sum += s_red[w];
-        l = l * f + sum;
-        m = m_new;
-        for (int i = 0; i < 2; ++i) {
-            const int e = t + i * kTile;
-            if (e >= a.dv) continue;
-            float o = acc[i] * f;
-            for (int k = 0; k < kTile; ++k)
-                if (s_row[k] >= 0) o += s_p[k] * elem(a.c, s_row[k], s_scale[k], e);
-            acc[i] = o;
-        }
-    }
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    const int64_t o = (row * a.h + head) * a.dv;
-    for (int i = 0; i < 2; ++i) {
-        const int e = t + i * kTile;
-        if (e < a.dv) reinterpret_cast<__nv_bfloat16 *>(a.out)[o + e] = __float2bfloat16_rn(acc[i] * inv);
-    }
-    if (t == 0 && a.lse) a.lse[row * a.h + head] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+    if (p >= cap && a.err_flag) atomicCAS(a.err_flag, 0, kCacheInval);
+    return p < end ? p : -1;
 }
+
+// ------------------------------------------------------------------------------------ staging rows
+// Warp lw of 8 stages positions 16 lw .. 16 lw + 15 of each tile.
+struct Loader {
+    const Kargs &k;
+    const Work &w;
+    Misc *m;
+    int64_t keys, end, cap;  // positions (or list entries) of the CTA's rows
+    int lane, lw;
+
+    struct Rows {
+        int64_t row, scale;  // element offsets of the lane's position (lane mod 16); row -1: none
+    };
+
+    __device__ __forceinline__ Rows find(int tile) const
+    {
+        Rows r{-1, 0};
+        const int64_t j = static_cast<int64_t>(tile) * kTile + lw * 16 + (lane & 15);
+        if (j < keys) {
+            const int64_t pos = k.a.idx ? listed(k.a, w.row0, j, end, cap) : j;
+            int64_t page, place;
+            if (pos >= 0) {
+                if (find_row(k.a.c, k.a.t, w.seq, pos, page, place)) {
+                    r.row = page * k.a.c.page_stride + place * k.a.c.row_stride;
+                    r.scale = page * k.a.c.scale_page_stride + place * k.a.c.scale_row_stride;
+                } else if (k.a.err_flag) {
+                    atomicCAS(k.a.err_flag, 0, kCacheInval);
+                }
+            }
+        }
+        return r;
+    }
+
+    // This warp's 16 validity bits of a tile.
+    __device__ __forceinline__ void note(int it, const Rows &r) const
+    {
+        const uint32_t bits = __ballot_sync(0xffffffffu, r.row >= 0) & 0xffffu;
+        if (lane == 0) reinterpret_cast<uint16_t *>(m->valid[it & (kValidSlots - 1)])[lw] = static_cast<uint16_t>(bits);
+    }
+};
+
+template <int C>
+__device__ __forceinline__ void load_bf16(const Loader &l, const Waiter &wait, unsigned char *ring, int lo, int hi)
+{
+    constexpr int R = Cfg<C>::ring;
+    constexpr int kBehind = R - 1 < 2 ? R - 1 : 2;  // chunks whose copies may still be in flight
+    Misc *m = l.m;
+    const uint16_t *data = static_cast<const uint16_t *>(l.k.a.c.data);
+    const int vec = l.lane & 15, d = l.k.a.d;
+    int told = 0;
+    const int total = (hi - lo) * C;
+    Loader::Rows next = l.find(lo);
+    for (int g = 0; g < total; ++g) {
+        const int it = g / C, c = g - it * C;
+        static_assert(kBehind >= 1, "");
+        const int stage = g % R;
+        if (g >= R) {
+            const int parity = (g / R - 1) & 1;
+            if (!__all_sync(0xffffffffu, mbar_try_wait(&m->empty[stage], parity, 0))) {
+                cp_async_wait<0>();
+                fence_proxy_async_shared();
+                __syncwarp();
+                for (; told < g; ++told)
+                    if (l.lane == 0) mbar_arrive(&m->full[told % R]);
+                wait(&m->empty[stage], parity);
+            }
+        }
+        Loader::Rows cur = next;
+        if (c == 0) l.note(it, cur);
+        if (c == C - 1) next = it + 1 < hi - lo ? l.find(lo + it + 1) : Loader::Rows{-1, 0};
+        const uint32_t base = smem_addr(ring + stage * kChunkBytes) + (vec >> 3) * kHalfBytes;
+        const bool in = c * 128 + vec * 8 < d;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int key = 2 * i + (l.lane >> 4);
+            const int64_t row = __shfl_sync(0xffffffffu, cur.row, key);
+            const int line = l.lw * 16 + key;
+            const bool ok = in && row >= 0;
+            cp_async16(base + line * 128 + (((vec & 7) ^ (line & 7)) << 4), data + (ok ? row + c * 128 + vec * 8 : 0),
+                       ok ? 16u : 0u);
+        }
+        cp_async_commit();
+        if (g - told >= kBehind) {
+            cp_async_wait<kBehind>();
+            fence_proxy_async_shared();
+            __syncwarp();
+            if (l.lane == 0) mbar_arrive(&m->full[told % R]);
+            ++told;
+        }
+    }
+    cp_async_wait<0>();
+    fence_proxy_async_shared();
+    __syncwarp();
+    for (; told < total; ++told)
+        if (l.lane == 0) mbar_arrive(&m->full[told % R]);
+}
+
+// 16 codes times their scale -> 16 bf16 in two 16-byte units.
+__device__ __forceinline__ void decode16(uint4 codes, float scale, uint4 &a, uint4 &b)
+{
+    const uint32_t in[4] = {codes.x, codes.y, codes.z, codes.w};
+    uint32_t out[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
+            static_cast<__nv_fp8x2_storage_t>((in[i >> 1] >> (16 * (i & 1))) & 0xffffu), __NV_E4M3);
+        const float2 f = __half22float2(__half2(h));
+        out[i] = pack_bf16(f.x * scale, f.y * scale);
+    }
+    a = make_uint4(out[0], out[1], out[2], out[3]);
+    b = make_uint4(out[4], out[5], out[6], out[7]);
+}
+
+template <int C>
+struct CodeChunk {
+    uint4 codes[4];
+    float scale[4];
+};
+
+template <int C>
+__device__ __forceinline__ void load_fp8(const Loader &l, const Waiter &wait, unsigned char *ring, int lo, int hi)
+{
+    constexpr int R = Cfg<C>::ring;
+    Misc *m = l.m;
+    const uint8_t *data = static_cast<const uint8_t *>(l.k.a.c.data);
+    const float *scales = l.k.a.c.scales;
+    const int vec = l.lane & 7, d = l.k.a.d;
+    const int total = (hi - lo) * C;
+    Loader::Rows cur{-1, 0}, next = l.find(lo);
+    int fetched = 0, fc = 0, ft = 0;  // next chunk to fetch, its column chunk and tile
+    auto fetch = [&](CodeChunk<C> &x) {
+        if (fetched >= total) return;
+        if (fc == 0) {
+            cur = next;
+            l.note(ft, cur);
+            next = ft + 1 < hi - lo ? l.find(lo + ft + 1) : Loader::Rows{-1, 0};
+        }
+        const bool in = fc * 128 + vec * 16 < d;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int key = 4 * i + (l.lane >> 3);
+            const int64_t row = __shfl_sync(0xffffffffu, cur.row, key);
+            const int64_t srow = __shfl_sync(0xffffffffu, cur.scale, key);
+            x.codes[i] = make_uint4(0u, 0u, 0u, 0u);
+            x.scale[i] = 0.0f;
+            if (in && row >= 0) {
+                x.codes[i] = *reinterpret_cast<const uint4 *>(data + row + fc * 128 + vec * 16);
+                x.scale[i] = scales[srow + fc];
+            }
+        }
+        ++fetched;
+        if (++fc == C) fc = 0, ++ft;
+    };
+    auto store = [&](int g, const CodeChunk<C> &x) {
+        if (g >= total) return;
+        const int stage = g % R;
+        if (g >= R) wait(&m->empty[stage], (g / R - 1) & 1);
+        unsigned char *base = ring + stage * kChunkBytes + (vec >> 2) * kHalfBytes;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int line = l.lw * 16 + 4 * i + (l.lane >> 3);
+            uint4 a, b;
+            decode16(x.codes[i], x.scale[i], a, b);
+            const int u = (2 * vec) & 7, sw = line & 7;
+            // lanes of the second half store their second unit first: the 8 lanes of a line then
+            // cover all banks in each of the two stores
+            const bool odd = vec >= 4;
+            *reinterpret_cast<uint4 *>(base + line * 128 + (((u + odd) ^ sw) << 4)) = odd ? b : a;
+            *reinterpret_cast<uint4 *>(base + line * 128 + (((u + !odd) ^ sw) << 4)) = odd ? a : b;
+        }
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (l.lane == 0) mbar_arrive(&m->full[stage]);
+    };
+    CodeChunk<C> x, y;
+    fetch(x);
+    fetch(y);
+    for (int g = 0; g < total; g += 2) {
+        store(g, x);
+        fetch(x);
+        store(g + 1, y);
+        fetch(y);
+    }
+}
+
+// ------------------------------------------------------------------------------------ issuing products
+template <int C>
+__device__ __forceinline__ void issue_products(const Kargs &k, Misc *m, const Waiter &wait, unsigned char *smem, int n)
+{
+    constexpr int R = Cfg<C>::ring;
+    constexpr uint32_t kScores = umma_idesc(kTile, kCols, false, false);
+    constexpr uint32_t kValues = umma_idesc(128, kCols, true, true);
+    const uint32_t ring = smem_addr(smem), q = smem_addr(smem + Cfg<C>::q_off), p = smem_addr(smem + Cfg<C>::p_off);
+    const uint32_t o_col = m->tmem, s_col = m->tmem + C * kCols;
+    const int vchunks = (k.a.dv + 127) >> 7;
+    const int steps_all = (k.a.d + 15) >> 4;  // steps of 16 elements; the rest of the last chunk is zeros
+    wait(&m->q_full, 0);
+    auto scores = [&](int it) {
+        const int buf = it & 1;
+        if (it >= 2) wait(&m->s_empty[buf], ((it >> 1) - 1) & 1);
+        tmem_fence_after();
+        for (int c = 0; c < C; ++c) {
+            const int g = it * C + c, stage = g % R;
+            wait(&m->full[stage], (g / R) & 1);
+            tmem_fence_after();
+            const int steps = min(8, steps_all - c * 8);
+            const uint32_t a0 = ring + stage * kChunkBytes, b0 = q + c * 2 * kQHalf;
+            for (int s = 0; s < steps; ++s) {
+                const uint64_t a = umma_desc(a0 + (s >> 2) * kHalfBytes + (s & 3) * 32, 16, 1024);
+                const uint64_t b = umma_desc(b0 + (s >> 2) * kQHalf + (s & 3) * 32, 16, 1024);
+                umma_bf16(s_col + buf * kCols, a, b, kScores, c > 0 || s > 0);
+            }
+        }
+        umma_commit(&m->s_full[buf]);
+    };
+    auto values = [&](int it) {
+        wait(&m->p_full[it & 1], (it >> 1) & 1);
+        tmem_fence_after();
+        const uint32_t b0 = p + (it % Cfg<C>::pbufs) * kPBytes;
+        for (int c = 0; c < C; ++c) {
+            const int stage = (it * C + c) % R;
+            if (c < vchunks) {
+                const uint32_t a0 = ring + stage * kChunkBytes;
+                for (int s = 0; s < kTile / 16; ++s) {
+                    const uint64_t a = umma_desc(a0 + s * 2048, kHalfBytes, 1024);
+                    const uint64_t b = umma_desc(b0 + s * 2048, kHalfBytes, 1024);
+                    umma_bf16(o_col + c * kCols, a, b, kValues, it > 0 || s > 0);
+                }
+            }
+            umma_commit(&m->empty[stage]);
+        }
+        umma_commit(&m->pv_done[it & 1]);
+    };
+    scores(0);
+    for (int it = 0; it < n; ++it) {
+        if (Cfg<C>::ahead && it + 1 < n) scores(it + 1);
+        values(it);
+        if (!Cfg<C>::ahead && it + 1 < n) scores(it + 1);
+    }
+}
+
+// ------------------------------------------------------------------------------------ softmax
+// Sum over the warp's lanes of each of 32 values a lane holds; lane j gets the sum of value j.
+__device__ __forceinline__ float reduce32(float v[32], int lane)
+{
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) {
+        const bool up = (lane & s) != 0;
+#pragma unroll
+        for (int j = 0; j < s; ++j) {
+            const float send = up ? v[j] : v[j + s];
+            const float keep = up ? v[j + s] : v[j];
+            v[j] = keep + __shfl_xor_sync(0xffffffffu, send, s);
+        }
+    }
+    return v[0];
+}
+
+template <int C>
+__device__ __forceinline__ void softmax(const Kargs &k, const Work &w, Misc *m, const Waiter &wait, unsigned char *smem,
+                                        int lo, int n, int warp, int lane)
+{
+    const int wg = warp >> 2, quad = warp & 3, line = quad * 32 + lane;
+    const int bar = 1 + wg;
+    const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
+    const uint32_t o_tm = m->tmem + lanes + wg * 32, s_tm = m->tmem + lanes + C * kCols + wg * 32;
+    const int vchunks = (k.a.dv + 127) >> 7;
+    const float scale = k.a.scale_log2;
+    const float4 *ref4 = reinterpret_cast<const float4 *>(m->ref + wg * 32);
+    const float4 *fac4 = reinterpret_cast<const float4 *>(m->factor + wg * 32);
+    const int *ends = m->end + wg * 32;
+    unsigned char *pbase = smem + Cfg<C>::p_off + line * 128;
+    float l[32];
+#pragma unroll
+    for (int j = 0; j < 32; ++j) l[j] = 0.0f;
+
+    for (int it = 0; it < n; ++it) {
+        const int buf = it & 1;
+        wait(&m->s_full[buf], (it >> 1) & 1);
+        tmem_fence_after();
+        uint32_t raw[32];
+        tmem_ld32(s_tm + buf * kCols, raw);
+        tmem_wait_ld();
+        tmem_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&m->s_empty[buf]);
+        const bool valid = (m->valid[it & (kValidSlots - 1)][quad] >> lane) & 1u;
+        const int pos = (lo + it) * kTile + line;
+        // a tile some of whose positions are past the end of some, not all, of the CTA's rows
+        const bool edges = !k.a.idx && pos - line + kTile > m->range[0] && m->range[0] < m->range[1];
+        bool dirty = false;
+        if (edges) {
+            // A position that one row attends to and another does not has weight 0 in the other, but
+            // 0 * NaN is NaN: a row that is not finite is taken out of the values, and the columns that
+            // do attend to it become NaN by their weight.  Such a row makes its score not finite.
+            const float s0 = __uint_as_float(raw[0]);
+            const bool odd = valid && !(fabsf(s0) < INFINITY);
+            if (bar_any(3, kSoftWarps * 32, odd)) {
+                if (odd)
+                    for (int e = 0; e < k.a.dv; ++e) {
+                        const unsigned char *at = smem + ((it * C + (e >> 7)) % Cfg<C>::ring) * kChunkBytes +
+                                                  ((e >> 6) & 1) * kHalfBytes + line * 128 +
+                                                  ((((e >> 3) & 7) ^ (line & 7)) << 4) + (e & 7) * 2;
+                        dirty |= (*reinterpret_cast<const uint16_t *>(at) & 0x7f80u) == 0x7f80u;
+                    }
+                bar_sync(3, kSoftWarps * 32);
+                if (dirty && wg == 0)
+                    for (int e = 0; e < k.a.dv; e += 8) {
+                        unsigned char *at = smem + ((it * C + (e >> 7)) % Cfg<C>::ring) * kChunkBytes +
+                                            ((e >> 6) & 1) * kHalfBytes + line * 128 +
+                                            ((((e >> 3) & 7) ^ (line & 7)) << 4);
+                        *reinterpret_cast<uint4 *>(at) = make_uint4(0u, 0u, 0u, 0u);
+                    }
+            }
+        }
+        float x[32];
+        bool over = false;
+#pragma unroll
+        for (int j4 = 0; j4 < 8; ++j4) {
+            const float4 r = ref4[j4];
+            const float rr[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+            for (int jj = 0; jj < 4; ++jj) {
+                const int j = j4 * 4 + jj;
+                float s = __uint_as_float(raw[j]) * scale;
+                if (edges && pos >= ends[j]) s = -INFINITY;
+                s = valid ? s : -INFINITY;
+                x[j] = s;
+                over |= s > rr[jj] + kRefSlack;
+            }
+        }
+        // (a column without positions yet has the reference -inf, which any score exceeds)
+        if (bar_any(bar, 128, over)) {
+            int top = 0;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+                const int t = __reduce_max_sync(0xffffffffu, order_of(x[j]));
+                top = lane == j ? t : top;
+            }
+            m->wmax[wg][quad][lane] = top;
+            bar_sync(bar, 128);
+            if (quad == 0) {
+                const int t = max(max(m->wmax[wg][0][lane], m->wmax[wg][1][lane]),
+                                  max(m->wmax[wg][2][lane], m->wmax[wg][3][lane]));
+                const float old = m->ref[wg * 32 + lane], now = fmaxf(old, float_of(t));
+                m->factor[wg * 32 + lane] = old == now ? 1.0f : exp2_approx(old - now);
+                m->ref[wg * 32 + lane] = now;
+            }
+            bar_sync(bar, 128);
+            if (it > 0) {
+                wait(&m->pv_done[(it - 1) & 1], ((it - 1) >> 1) & 1);
+                tmem_fence_after();
+                for (int c = 0; c < vchunks; ++c) {
+                    tmem_ld32(o_tm + c * kCols, raw);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        raw[j] = __float_as_uint(__uint_as_float(raw[j]) * reinterpret_cast<const float *>(fac4)[j]);
+                    tmem_st32(o_tm + c * kCols, raw);
+                }
+                tmem_wait_st();
+            }
+#pragma unroll
+            for (int j = 0; j < 32; ++j) l[j] *= reinterpret_cast<const float *>(fac4)[j];
+        }
+        // the buffer of P is free once the product that read it is done
+        if (it >= Cfg<C>::pbufs) {
+            const int before = it - Cfg<C>::pbufs;
+            wait(&m->pv_done[before & 1], (before >> 1) & 1);
+        }
+        unsigned char *prow = pbase + (it % Cfg<C>::pbufs) * kPBytes;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            float pr[8];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float4 r = ref4[u * 2 + h];
+                const float rr[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+                for (int jj = 0; jj < 4; ++jj) {
+                    const int j = u * 8 + h * 4 + jj;
+                    // a masked score is -inf, also where the column has no reference yet
+                    float p = x[j] == -INFINITY ? 0.0f : exp2_approx(x[j] - rr[jj]);
+                    if (dirty && pos < ends[j]) p = __int_as_float(0x7fffffff);
+                    pr[h * 4 + jj] = p;
+                    l[j] += p;
+                }
+            }
+            *reinterpret_cast<uint4 *>(prow + (((wg * 4 + u) ^ (line & 7)) << 4)) =
+                make_uint4(pack_bf16(pr[0], pr[1]), pack_bf16(pr[2], pr[3]), pack_bf16(pr[4], pr[5]),
+                           pack_bf16(pr[6], pr[7]));
+        }
+        fence_proxy_async_shared();
+        tmem_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&m->p_full[it & 1]);
+    }
+
+    // column sums, in a fixed order
+    m->lsum[quad][wg * 32 + lane] = reduce32(l, lane);
+    bar_sync(bar, 128);
+    const int col = wg * 32 + lane;
+    const float sum = (m->lsum[0][col] + m->lsum[1][col]) + (m->lsum[2][col] + m->lsum[3][col]);
+    const bool used = col < w.cols();
+    const int64_t out_row = (w.row0 + col / w.heads) * k.a.h + w.head0 + col % w.heads;  // of lane's column
+    if (quad == 0) {
+        m->inv[col] = sum == 0.0f ? 0.0f : 1.0f / sum;
+        if (used) {
+            if (k.p.parts > 1)
+                k.part_ml[out_row * k.p.parts + w.part] = make_float2(m->ref[col], sum);
+            else if (k.a.lse)
+                k.a.lse[out_row] = sum == 0.0f ? -INFINITY : (m->ref[col] + log2f(sum)) * 0.69314718055994531f;
+        }
+    }
+    bar_sync(bar, 128);
+    if (n > 0) {
+        wait(&m->pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1);
+        tmem_fence_after();
+    }
+    const int cols = w.cols();
+    if (k.p.parts > 1) {
+        if (n == 0) return;  // a part without positions has the sum 0: its accumulators are not read
+        for (int c = 0; c < vchunks; ++c) {
+            uint32_t o[32];
+            tmem_ld32(o_tm + c * kCols, o);
+            tmem_wait_ld();
+            const int e = c * 128 + line;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+                const int64_t r = __shfl_sync(0xffffffffu, out_row, j);
+                if (wg * 32 + j < cols && e < k.a.dv) k.part_o[(r * k.p.parts + w.part) * k.a.dv + e] = __uint_as_float(o[j]);
+            }
+        }
+        return;
+    }
+    // the group's 32 columns x 128 elements through its half of a P buffer (free by now), so that whole
+    // 16-byte vectors of a column are written
+    unsigned char *stage = smem + Cfg<C>::p_off + wg * (kPBytes / 2);
+    for (int c = 0; c < vchunks; ++c) {
+        uint32_t o[32];
+        if (n > 0) {
+            tmem_ld32(o_tm + c * kCols, o);
+            tmem_wait_ld();
+        } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] = 0u;
+        }
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+            const float v = __uint_as_float(o[j]) * m->inv[wg * 32 + j];
+            *reinterpret_cast<__nv_bfloat16 *>(stage + j * 256 + line * 2) = __float2bfloat16_rn(v);
+        }
+        bar_sync(bar, 128);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int j = quad * 8 + i * 2 + (lane >> 4), e = c * 128 + (lane & 15) * 8;
+            const int64_t r = __shfl_sync(0xffffffffu, out_row, j);
+            if (wg * 32 + j < cols && e < k.a.dv)
+                __stcs(reinterpret_cast<uint4 *>(k.a.out + r * k.a.dv + e),
+                       *reinterpret_cast<const uint4 *>(stage + j * 256 + (lane & 15) * 16));
+        }
+        bar_sync(bar, 128);
+    }
+}
+
+// ------------------------------------------------------------------------------------ the kernel
+template <int C, bool FP8>
+__global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_constant__ Kargs k)
+{
+    extern __shared__ __align__(1024) unsigned char smem[];
+    Misc *m = reinterpret_cast<Misc *>(smem + Cfg<C>::misc_off);
+    const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+    const Work w = work_of(k);
+    const int64_t cap = k.a.t.max_pages * k.a.c.page_size;
+    if (t == 0) {
+        for (int i = 0; i < Cfg<C>::ring; ++i) {
+            mbar_init(&m->full[i], kLoadWarps);
+            mbar_init(&m->empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&m->s_full[i], 1);
+            mbar_init(&m->s_empty[i], kSoftWarps);
+            mbar_init(&m->p_full[i], kSoftWarps);
+            mbar_init(&m->pv_done[i], 1);
+        }
+        mbar_init(&m->q_full, kSoftWarps);
+        fence_mbar_init();
+        m->abort = 0;
+        m->last = 0;
+        m->range[0] = 0x7fffffff;
+        m->range[1] = 0;
+    }
+    if (warp == kMmaWarp) tmem_alloc(&m->tmem, 512);
+    __syncthreads();
+    if (t < kCols) {
+        int e = 0;
+        if (t < w.cols()) {
+            const int64_t row = w.row0 + t / w.heads;
+            int64_t v = k.a.end ? k.a.end[row] : cap;
+            v = v < 0 ? 0 : (v > cap ? cap : v);
+            e = static_cast<int>(v);
+            atomicMin(&m->range[0], e);
+            atomicMax(&m->range[1], e);
+        }
+        m->end[t] = e;
+        m->ref[t] = -INFINITY;
+        m->factor[t] = 1.0f;
+    }
+    if (k.a.idx) {
+        int64_t e = k.a.end ? k.a.end[w.row0] : cap;
+        e = e > cap ? cap : e;
+        int last = 0;
+        for (int j = t; j < k.a.n; j += kThreads)
+            if (listed(k.a, w.row0, j, e, cap) >= 0) last = j + 1;
+        last = __reduce_max_sync(0xffffffffu, last);
+        if (lane == 0 && last > 0) atomicMax(&m->last, last);
+    }
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    const int64_t keys = k.a.idx ? m->last : m->range[1];
+    const int64_t tiles = (keys + kTile - 1) / kTile;
+    const int lo = static_cast<int>(tiles * w.part / k.p.parts), hi = static_cast<int>(tiles * (w.part + 1) / k.p.parts);
+    const int n = hi - lo;
+    const Waiter wait{&m->abort, k.a.err_flag};
+
+    if (warp < kSoftWarps) {
+        regs_up<kSoftRegs>();
+        if (n > 0) {
+            // the CTA's queries; unused columns and elements past d are zeros
+            unsigned char *q = smem + Cfg<C>::q_off;
+            for (int i = t; i < kCols * C * 16; i += kSoftWarps * 32) {
+                const int col = i / (C * 16), vec = i - col * (C * 16);
+                uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                if (col < w.cols() && vec * 8 < k.a.d) {
+                    const int64_t row = w.row0 + col / w.heads;
+                    const int head = w.head0 + col % w.heads;
+                    v = *reinterpret_cast<const uint4 *>(k.a.q + row * k.a.q_row_stride + head * k.a.q_head_stride +
+                                                         vec * 8);
+                }
+                *reinterpret_cast<uint4 *>(q + (vec >> 3) * kQHalf + col * 128 + (((vec & 7) ^ (col & 7)) << 4)) = v;
+            }
+            fence_proxy_async_shared();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&m->q_full);
+        }
+        softmax<C>(k, w, m, wait, smem, lo, n, warp, lane);
+    } else if (warp < kLoadWarp0) {
+        regs_down<kMmaRegs>();
+        if (warp == kMmaWarp && n > 0 && lane == 0) issue_products<C>(k, m, wait, smem, n);
+        __syncwarp();
+    } else {
+        regs_down<kLoadRegs>();
+        int64_t e = k.a.end ? k.a.end[w.row0] : cap;  // selected positions: the row's own end
+        e = e > cap ? cap : e;
+        const Loader l{k, w, m, keys, e, cap, lane, warp - kLoadWarp0};
+        if (n > 0) {
+            if (FP8)
+                load_fp8<C>(l, wait, smem, lo, hi);
+            else
+                load_bf16<C>(l, wait, smem, lo, hi);
+        }
+    }
+    tmem_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) tmem_dealloc(m->tmem, 512);
+}
+
+// Joins the parts of each (row, head): out = sum_p 2^(ref_p - max) o_p / sum_p 2^(ref_p - max) sum_p.
+__global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Kargs k)
+{
+    const int64_t item = blockIdx.x;
+    const int parts = k.p.parts, dv = k.a.dv;
+    const float2 *ml = k.part_ml + item * parts;
+    float top = -INFINITY;
+    for (int p = 0; p < parts; ++p) {
+        const float2 v = ml[p];
+        if (v.y != 0.0f) top = fmaxf(top, v.x);
+    }
+    float sum = 0.0f;
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    const int e = threadIdx.x * 4;
+    for (int p = 0; p < parts; ++p) {
+        const float2 v = ml[p];
+        if (v.y == 0.0f) continue;
+        const float f = v.x == top ? 1.0f : exp2_approx(v.x - top);
+        sum += f * v.y;
+        if (e < dv) {
+            const float4 o = *reinterpret_cast<const float4 *>(k.part_o + (item * parts + p) * dv + e);
+            acc.x += f * o.x, acc.y += f * o.y, acc.z += f * o.z, acc.w += f * o.w;
+        }
+    }
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    if (e < dv)
+        *reinterpret_cast<uint2 *>(k.a.out + item * dv + e) =
+            make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+    if (threadIdx.x == 0 && k.a.lse) k.a.lse[item] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
+}
+
+template <int C, bool FP8>
+cudaError_t launch(const Kargs &k, cudaStream_t s)
+{
+    constexpr size_t smem = Cfg<C>::misc_off + sizeof(Misc);
+    static_assert(smem <= 232448, "more than a CTA may use");
+    static_assert(smem > 116 * 1024, "one CTA an SM: each takes all of the tensor memory");
+    cudaError_t e = cudaFuncSetAttribute(attention_kernel<C, FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    const dim3 grid(static_cast<unsigned>(k.p.items), static_cast<unsigned>(k.p.parts));
+    attention_kernel<C, FP8><<<grid, kThreads, smem, s>>>(k);
+    return cudaGetLastError();
+}
+
+Plan plan_of(int64_t rows, int64_t h, int64_t b, int64_t positions, bool idx_given)
+{
+    Plan p{};
+    const int64_t per = rows / b;
+    p.heads_per_tile = static_cast<int>(h < kCols ? h : kCols);
+    p.head_blocks = static_cast<int>((h + kCols - 1) / kCols);
+    // rows that share a tile share its positions; a row with a list has its own
+    const int64_t fit = idx_given ? 1 : kCols / p.heads_per_tile;
+    p.rows_per_tile = static_cast<int>(fit < per ? fit : per);
+    p.tiles_per_seq = (per + p.rows_per_tile - 1) / p.rows_per_tile;
+    p.items = b * p.tiles_per_seq * p.head_blocks;
+    // parts: as many as keep the fewest tiles in a row, counting a part's start and end as 1.5 tiles
+    const int64_t tiles = (positions + kTile - 1) / kTile;
+    const int64_t sms = device_sm_count() > 0 ? device_sm_count() : 1;
+    p.parts = 1;
+    double best = 0.0;
+    for (int64_t n = 1; n <= kMaxSplit && n <= (tiles > 1 ? tiles : 1); ++n) {
+        const int64_t waves = (p.items * n + sms - 1) / sms;
+        const double cost = static_cast<double>(waves) * (static_cast<double>((tiles + n - 1) / n) + 1.5) + (n > 1 ? 1.0 : 0.0);
+        if (n == 1 || cost < best) {
+            best = cost;
+            p.parts = static_cast<int>(n);
+        }
+        if (p.items * n > 2 * sms) break;
+    }
+    return p;
+}
+
+size_t part_bytes(int64_t items, int parts) { return static_cast<size_t>((items * parts * 8 + 255) / 256 * 256); }
 
 }  // namespace
 
-size_t cache_attention_workspace(int64_t, int64_t, int64_t, int64_t, int64_t, int64_t, bool) { return 0; }
+size_t cache_attention_workspace(int64_t rows, int64_t h, int64_t, int64_t dv, int64_t b, int64_t positions,
+                                 bool idx_given)
+{
+    const Plan p = plan_of(rows, h, b, positions, idx_given);
+    if (p.parts == 1) return 0;
+    return part_bytes(rows * h, p.parts) + static_cast<size_t>(rows * h) * p.parts * dv * 4;
+}
 
 cudaError_t launch_cache_attention(const CacheAttnArgs &a, cudaStream_t s)
 {
-    if (a.rows > 0x7fffffffLL || a.h > 65535) return cudaErrorInvalidValue;
-    attention_plain_kernel<<<dim3(static_cast<unsigned>(a.rows), static_cast<unsigned>(a.h)), kTile, 0, s>>>(a);
+    Kargs k{};
+    k.a = a;
+    k.p = plan_of(a.rows, a.h, a.rows / a.t.rows_per_seq, a.idx ? a.n : a.t.max_pages * a.c.page_size, a.idx != nullptr);
+    if (k.p.items > 0x7fffffffLL) return cudaErrorInvalidValue;
+    if (k.p.parts > 1) {
+        k.part_ml = static_cast<float2 *>(a.ws);
+        k.part_o = reinterpret_cast<float *>(static_cast<unsigned char *>(a.ws) + part_bytes(a.rows * a.h, k.p.parts));
+    }
+    const bool fp8 = a.c.scales != nullptr;
+    cudaError_t e;
+    switch ((a.d + 127) / 128) {
+    case 1: e = fp8 ? launch<1, true>(k, s) : launch<1, false>(k, s); break;
+    case 2: e = fp8 ? launch<2, true>(k, s) : launch<2, false>(k, s); break;
+    case 3: e = fp8 ? launch<3, true>(k, s) : launch<3, false>(k, s); break;
+    default: e = fp8 ? launch<4, true>(k, s) : launch<4, false>(k, s); break;
+    }
+    if (e != cudaSuccess || k.p.parts == 1) return e;
+    join_kernel<<<static_cast<unsigned>(a.rows * a.h), 128, 0, s>>>(k);
     return cudaGetLastError();
 }
 

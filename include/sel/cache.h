@@ -100,7 +100,8 @@ SEL_API int sel_cache_gather(const sel_cache *cache, const int32_t *page_table, 
  * Positions past the page table, or whose page is not in [0, pages), are left
  * out and set *err_flag = SEL_EINVAL.  Sums and the softmax are in fp32; the
  * weights are rounded to bf16 for the product with the values.
- * SEL_EUNSUPPORTED: d > SEL_CACHE_ATTN_MAX_D, or sizes past 2^31 - 1. */
+ * SEL_EUNSUPPORTED: d > SEL_CACHE_ATTN_MAX_D, rows * h > 2^31 - 1, or
+ * n or max_pages * page_size > 2^31 - 256. */
 SEL_API int sel_cache_attention(const void *q, int64_t rows, int64_t h, int64_t q_row_stride, int64_t q_head_stride,
                                 const sel_cache *cache, const int32_t *page_table, int64_t b, int64_t max_pages,
                                 int64_t table_stride, const int32_t *end, const void *idx, int idx_dtype, int64_t n,
