@@ -34,20 +34,11 @@
 namespace sel {
 namespace {
 
-constexpr int kCols = 64;                  // (row, head) columns of a CTA
-constexpr int kTile = 128;                 // positions of a tile
-constexpr int kChunkBytes = kTile * 256;   // 128 positions x 128 columns of bf16
-constexpr int kHalfBytes = kChunkBytes / 2;  // 64 columns: one 128-byte line a position
-constexpr int kQHalf = kCols * 128;        // 64 query columns x 64 elements
-constexpr int kPBytes = kTile * 128;       // P^T: 128 positions x 64 columns
-constexpr int kSoftWarps = 8, kLoadWarps = 8;
-constexpr int kMmaWarp = kSoftWarps;           // its group of 4 warps holds two that work:
-constexpr int kUnitWarp = kMmaWarp + 1;        // the one that issues and the one that looks up what is next
+constexpr int kMaxCols = 128;              // (row, head) columns of a CTA at most
+constexpr int kSoftWarps = 16;             // four groups of 4 warps, a quarter of the columns each
+constexpr int kMmaWarp = kSoftWarps;       // the one that issues, in a group of 4 with
+constexpr int kUnitWarp = kMmaWarp + 1;    // the one that looks up what is next and two that stage queries
 constexpr int kLoadWarp0 = kSoftWarps + 4;
-constexpr int kThreads = (kLoadWarp0 + kLoadWarps) * 32;
-// Registers a thread after the roles part, out of the 640 x 96 of the launch:
-// 256 x 136 + 128 x 48 + 256 x 80 = 61440.
-constexpr int kSoftRegs = 136, kMmaRegs = 48, kLoadRegs = 80;
 constexpr int kMaxRing = 5;
 constexpr int kValidSlots = 16;            // tiles whose validity bits are kept (more than the ring holds)
 constexpr int kMaxSplit = 64;
@@ -56,14 +47,39 @@ constexpr long long kWaitCycles = 4000000000LL;  // about 2 s
 constexpr uint32_t kSuspend = 1000;
 constexpr int32_t kTimeout = 5;            // SEL_ETIMEOUT
 
-template <int C>
+// C chunks of 128 elements a row, N columns.  Measured tensor rates: 128 x 64 x 16 takes 48.7 cycles
+// (66% of the peak: reading the operands from shared memory bounds it), 128 x 128 x 16 takes 64.6 (99%).
+// So 128 columns are taken where queries, P and two tiles of rows fit beside one another: rows of up to 192
+// elements.  (64-position tiles, two of which fit for rows of 512 elements, take 45.4 for 64 x 64 x 16, and
+// were measured slower: 716 against 532 us for 4096 rows of 64 heads over 512 selected positions.)
+template <int C, int N>
 struct Cfg {
-    static constexpr int ring = C <= 1 ? 5 : 4;          // chunks staged
-    static constexpr int pbufs = C <= 2 ? 2 : 1;
-    static constexpr bool ahead = ring >= 2 * C;         // the next tile's scores before this one's values
-    static constexpr int q_off = ring * kChunkBytes;
-    static constexpr int p_off = q_off + C * 2 * kQHalf;
-    static constexpr int misc_off = p_off + pbufs * kPBytes;
+    static_assert(N == 64 || N == 128, "");
+    static constexpr bool wide = N == 128;
+    static constexpr int M = 128;                                   // positions of a tile
+    static constexpr int half_bytes = M * 128;                      // a tile's 64 columns: one 128-byte line a position
+    static constexpr int chunk_bytes = 2 * half_bytes;
+    static constexpr int q_halves = wide && C == 2 ? 3 : 2 * C;     // blocks of 64 elements of a query
+    static constexpr int q_half = N * 128;                          // bytes of one
+    static constexpr int p_block = M * 128;                         // 64 columns of P^T, a line a position
+    static constexpr int p_bytes = N / 64 * p_block;
+    static constexpr int ring = wide && C == 1 ? 3 : (C == 1 ? 5 : 4);  // chunks staged
+    static constexpr int pbufs = C == 1 || (C == 2 && !wide) ? 2 : 1;
+    static constexpr bool ahead = ring >= 2 * C;  // the next tile's scores before this one's values
+    static constexpr int q_off = ring * chunk_bytes;
+    static constexpr int p_off = q_off + q_halves * q_half;
+    static constexpr int misc_off = p_off + pbufs * p_bytes;
+    static constexpr int cols_per_group = N / 4;
+    static constexpr int load_warps = wide ? 4 : 8;
+    static constexpr int threads = (kLoadWarp0 + load_warps) * 32;
+    // Registers a thread after the roles part, of 896 x 72 (768 x 80) at the launch:
+    // 512 x 64 + 128 x 40 + 256 x 96 = 62464 <= 64512;  512 x 88 + 128 x 40 + 128 x 88 = 61440.
+    static constexpr int launch_regs = wide ? 80 : 72;
+    static constexpr int soft_regs = wide ? 88 : 64;
+    static constexpr int mma_regs = 40;
+    static constexpr int load_regs = wide ? 88 : 96;
+    static_assert(ring >= C && ring <= kMaxRing, "");
+    static_assert(512 * soft_regs + 128 * mma_regs + 32 * load_warps * load_regs <= threads * launch_regs, "");
 };
 
 // What a CTA works on next, made by one warp ahead of the others.
@@ -75,7 +91,8 @@ struct Unit {
     int part;
     int lo, n;               // first tile and tiles
     int min_end, max_end;    // of its rows
-    alignas(16) int end[kCols];  // exclusive end of each column's row, 0 for unused columns
+    alignas(16) int end[kMaxCols];  // exclusive end of each column's row, 0 for unused columns
+    alignas(16) int out[kMaxCols];  // row * heads + head of each column
     __device__ __forceinline__ int cols() const { return rows * heads; }
 };
 
@@ -84,18 +101,14 @@ struct Misc {
     uint64_t unit_full[2], unit_empty[2];
     uint32_t tmem;
     int abort;
-    alignas(16) float ref[kCols];  // read 16 bytes at a time
-    alignas(16) float factor[kCols];
-    alignas(16) float inv[kCols];
-    alignas(16) float wmax[4][kCols];
-    alignas(16) float lsum[4][kCols];
+    alignas(16) float inv[kMaxCols];      // 1 / sum
+    alignas(16) float part[4][kMaxCols];  // maxima, then sums, of the four warps of a group
     alignas(16) uint32_t valid[kValidSlots][4];  // bit k of word w: position 32 w + k of the tile has a cache row
     alignas(16) Unit unit[2];
 };
-static_assert(offsetof(Misc, ref) % 16 == 0 && offsetof(Misc, factor) % 16 == 0 && offsetof(Misc, valid) % 16 == 0 &&
-                  offsetof(Misc, unit) % 16 == 0, "");
 
 struct Plan {
+    int cols;            // columns of a CTA: 64 or 128
     int rows_per_tile;   // T
     int heads_per_tile;  // heads of a head block
     int head_blocks;
@@ -153,6 +166,7 @@ __device__ __forceinline__ int64_t listed(const CacheAttnArgs &a, int64_t row, i
 }
 
 // One warp: unit u of the call.
+template <int N, int M>
 __device__ __forceinline__ void make_unit(const Kargs &k, int64_t u, Unit *w, int lane)
 {
     const int64_t cap = k.a.t.max_pages * k.a.c.page_size;
@@ -170,11 +184,13 @@ __device__ __forceinline__ void make_unit(const Kargs &k, int64_t u, Unit *w, in
     const int heads = min(k.p.heads_per_tile, k.a.h - head0);
     int least = 0x7fffffff, most = 0;
 #pragma unroll
-    for (int i = 0; i < kCols / 32; ++i) {
+    for (int i = 0; i < N / 32; ++i) {
         const int col = i * 32 + lane;
         int e = 0;
+        const int row = col / heads;
+        w->out[col] = static_cast<int>((row0 + row) * k.a.h) + head0 + col - row * heads;
         if (col < rows * heads) {
-            const int64_t v = k.a.end ? k.a.end[row0 + col / heads] : cap;
+            const int64_t v = k.a.end ? k.a.end[row0 + row] : cap;
             e = static_cast<int>(v < 0 ? 0 : (v > cap ? cap : v));
             least = min(least, e);
             most = max(most, e);
@@ -192,7 +208,7 @@ __device__ __forceinline__ void make_unit(const Kargs &k, int64_t u, Unit *w, in
         keys = __reduce_max_sync(0xffffffffu, last);
     }
     if (lane == 0) {
-        const int64_t tiles = (keys + kTile - 1) / kTile;
+        const int64_t tiles = (keys + M - 1) / M;
         w->row0 = row0;
         w->seq = seq;
         w->keys = keys;
@@ -209,228 +225,300 @@ __device__ __forceinline__ void make_unit(const Kargs &k, int64_t u, Unit *w, in
 }
 
 // ------------------------------------------------------------------------------------ staging rows
-// Warp lw of 8 stages positions 16 lw .. 16 lw + 15 of each tile.
+// 16 codes times their scale -> 16 bf16 in two 16-byte units.
+__device__ __forceinline__ void decode16(uint4 codes, float scale, uint4 &a, uint4 &b)
+{
+    const uint32_t in[4] = {codes.x, codes.y, codes.z, codes.w};
+    uint32_t out[8];
+    // A power of two below 2^8 and no NaN among the codes: the code's exponent and mantissa bits, put
+    // where bf16 has them, are the value times 2^-120 (subnormal codes give subnormal numbers), and one
+    // bf16 product makes it value * scale, rounding only where the result is subnormal.
+    const uint32_t s = __float_as_uint(scale);
+    uint32_t nan = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) nan |= (in[i] & 0x7f7f7f7fu) + 0x01010101u;
+    if ((s & 0x007fffffu) == 0 && s - 0x00800000u < (134u << 23) && (nan & 0x80808080u) == 0) {
+        const uint32_t f = (s >> 16) + (120u << 7), f2 = f | (f << 16);
+        const __nv_bfloat162 by = *reinterpret_cast<const __nv_bfloat162 *>(&f2);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            // bytes to sign-extended halves, shifted to the places of bf16's exponent and mantissa
+            uint32_t y;  // (selector digits from 8 repeat the byte's sign; __byte_perm drops that bit)
+            asm("prmt.b32 %0, %1, 0, %2;" : "=r"(y) : "r"(in[i >> 1]), "r"(i & 1 ? 0xb3a2 : 0x9180));
+            y = (y << 4) & 0x87f087f0u;
+            const __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&y), by);
+            out[i] = *reinterpret_cast<const uint32_t *>(&v);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
+                static_cast<__nv_fp8x2_storage_t>((in[i >> 1] >> (16 * (i & 1))) & 0xffffu), __NV_E4M3);
+            const float2 v = __half22float2(__half2(h));
+            out[i] = pack_bf16(v.x * scale, v.y * scale);
+        }
+    }
+    a = make_uint4(out[0], out[1], out[2], out[3]);
+    b = make_uint4(out[4], out[5], out[6], out[7]);
+}
+
+template <int C, int N, bool FP8>
 struct Loader {
+    using F = Cfg<C, N>;
+    // Warp lw stages positions lw * kPos .. of each tile: lane mod kPos looks one up, and the lanes of a
+    // line (16 of 16 bytes of bf16, 8 of 16 codes) keep the rows they copy in registers for the tile.
+    static constexpr int kPos = F::M / F::load_warps;  // 8, 16 or 32
+    static constexpr int kLanes = FP8 ? 8 : 16;        // lanes of a line
+    static constexpr int kVecs = kPos * kLanes / 32;   // lines a lane takes part in
     const Kargs &k;
     Misc *m;
-    const Unit *w;
-    int64_t cap;
+    const Waiter &wait;
+    unsigned char *smem;
     int lane, lw;
-    int stage, phase;  // of the ring; a fresh barrier's phase of parity 1 counts as completed
-    int tile;          // tiles staged so far
+    const Unit *w = nullptr;
+    int stage = 0, phase = 1;  // of the ring; a fresh barrier's phase of parity 1 counts as completed
+    int tile = 0;              // tiles staged so far
 
     struct Rows {
-        int64_t row, scale;  // element offsets of the lane's position (lane mod 16); row -1: none
+        int64_t row, scale;  // element offsets of the lane's position; row -1: none
     };
 
     // Of tile i of the unit.
     __device__ __forceinline__ Rows find(int i) const
     {
         Rows r{-1, 0};
-        const int64_t j = static_cast<int64_t>(w->lo + i) * kTile + lw * 16 + (lane & 15);
-        if (i < w->n && j < w->keys) {
-            const int64_t pos = k.a.idx ? listed(k.a, w->row0, j, w->list_end, cap) : j;
-            int64_t page, place;
-            if (pos >= 0) {
-                if (find_row(k.a.c, k.a.t, w->seq, pos, page, place)) {
-                    r.row = page * k.a.c.page_stride + place * k.a.c.row_stride;
-                    r.scale = page * k.a.c.scale_page_stride + place * k.a.c.scale_row_stride;
-                } else if (k.a.err_flag) {
-                    atomicCAS(k.a.err_flag, 0, kCacheInval);
-                }
-            }
+        const int64_t j = static_cast<int64_t>(w->lo + i) * F::M + lw * kPos + (lane & (kPos - 1));
+        if (i >= w->n || j >= w->keys) return r;
+        const int64_t pos = k.a.idx ? listed(k.a, w->row0, j, w->list_end, k.a.t.max_pages * k.a.c.page_size) : j;
+        if (pos < 0) return r;
+        int64_t page, place;
+        if (find_row(k.a.c, k.a.t, w->seq, pos, page, place)) {
+            r.row = page * k.a.c.page_stride + place * k.a.c.row_stride;
+            r.scale = page * k.a.c.scale_page_stride + place * k.a.c.scale_row_stride;
+        } else if (k.a.err_flag) {
+            atomicCAS(k.a.err_flag, 0, kCacheInval);
         }
         return r;
     }
 
-    // This warp's 16 validity bits of the next tile.
+    // This warp's validity bits of the next tile.
     __device__ __forceinline__ void note(const Rows &r)
     {
-        const uint32_t bits = __ballot_sync(0xffffffffu, r.row >= 0) & 0xffffu;
-        if (lane == 0)
-            reinterpret_cast<uint16_t *>(m->valid[tile & (kValidSlots - 1)])[lw] = static_cast<uint16_t>(bits);
+        const uint32_t bits = __ballot_sync(0xffffffffu, r.row >= 0);
+        uint32_t *to = m->valid[tile & (kValidSlots - 1)];
+        if (lane == 0) {
+            if (kPos == 32)
+                to[lw] = bits;
+            else if (kPos == 16)
+                reinterpret_cast<uint16_t *>(to)[lw] = static_cast<uint16_t>(bits);
+            else
+                reinterpret_cast<uint8_t *>(to)[lw] = static_cast<uint8_t>(bits);
+        }
         ++tile;
     }
 
-    // The unit's queries by all 256 threads; unused columns and elements past d are zeros.
-    template <int C>
-    __device__ __forceinline__ void queries(unsigned char *q) const
+    __device__ __forceinline__ void next_stage()
     {
-        const int vec = lane & 15, heads = w->heads, cols = w->cols();
-        const uint32_t to = smem_addr(q) + (vec >> 3) * kQHalf;
-#pragma unroll
-        for (int i = 0; i < kCols / 16; ++i) {
-            const int col = (i * kLoadWarps + lw) * 2 + (lane >> 4);
-            const int row = col / heads;
-            const uint16_t *src = k.a.q + (w->row0 + row) * k.a.q_row_stride +
-                                  static_cast<int64_t>(w->head0 + col - row * heads) * k.a.q_head_stride;
-#pragma unroll
-            for (int c = 0; c < C; ++c) {
-                const int e = c * 128 + vec * 8;
-                const bool ok = col < cols && e < k.a.d;
-                cp_async16(to + c * 2 * kQHalf + col * 128 + (((vec & 7) ^ (col & 7)) << 4), ok ? src + e : k.a.q,
-                           ok ? 16u : 0u);
-            }
-        }
-        cp_async_arrive(&m->q_full);
+        if (++stage == F::ring) stage = 0, phase ^= 1;
     }
-};
 
-template <int C>
-__device__ __forceinline__ void load_bf16(Loader &l, const Waiter &wait, unsigned char *ring)
-{
-    constexpr int R = Cfg<C>::ring;
-    Misc *m = l.m;
-    const uint16_t *data = static_cast<const uint16_t *>(l.k.a.c.data);
-    const int vec = l.lane & 15, d = l.k.a.d, n = l.w->n;
-    const int line0 = l.lw * 16 + (l.lane >> 4);
-    const uint32_t to = smem_addr(ring) + (vec >> 3) * kHalfBytes + line0 * 128;
-    Loader::Rows next = l.find(0);
-    for (int it = 0; it < n; ++it) {
-        const Loader::Rows cur = next;
-        l.note(cur);
-        next = l.find(it + 1);
+    // ---- bf16 rows: asynchronous copies, whose completion arrives at the chunk's barrier by itself.  (Waiting
+    // for them here instead keeps the warp from filling a chunk that has come free meanwhile.)
+    __device__ __forceinline__ void rows_bf16()
+    {
+        const uint16_t *data = static_cast<const uint16_t *>(k.a.c.data);
+        const int vec = lane & 15, d = k.a.d, n = w->n;
+        const int line0 = lw * kPos + (lane >> 4);
+        const uint32_t to = smem_addr(smem) + (vec >> 3) * F::half_bytes + line0 * 128;
+        const int halves = (d + 63) >> 6;
+        constexpr int V = kVecs < 8 ? kVecs : 8;
+        Rows next = find(0);
+        for (int it = 0; it < n; ++it) {
+            const Rows cur = next;
+            note(cur);
+            next = find(it + 1);
+            int64_t row[V];
+            if (kVecs <= 8) {
+#pragma unroll
+                for (int i = 0; i < V; ++i) row[i] = __shfl_sync(0xffffffffu, cur.row, 2 * i + (lane >> 4));
+            }
 #pragma unroll 1
-        for (int c = 0; c < C; ++c) {
-            wait(&m->empty[l.stage], l.phase);
-            const uint32_t base = to + l.stage * kChunkBytes;
-            const int e = c * 128 + vec * 8;
+            for (int c = 0; c < C; ++c) {
+                wait(&m->empty[stage], phase);
+                const uint32_t base = to + stage * F::chunk_bytes;
+                const int e = c * 128 + vec * 8;
+                const bool used = c * 2 + (vec >> 3) < halves;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int64_t row = __shfl_sync(0xffffffffu, cur.row, 2 * i + (l.lane >> 4));
-                const bool ok = e < d && row >= 0;
-                cp_async16(base + i * 256 + (((vec & 7) ^ ((line0 + 2 * i) & 7)) << 4), data + (ok ? row + e : 0),
-                           ok ? 16u : 0u);
+                for (int i = 0; i < kVecs; ++i) {
+                    const int64_t r = kVecs <= 8 ? row[i & (V - 1)] : __shfl_sync(0xffffffffu, cur.row, 2 * i + (lane >> 4));
+                    const bool ok = e < d && r >= 0;
+                    if (used)
+                        cp_async16(base + i * 256 + (((vec & 7) ^ ((line0 + 2 * i) & 7)) << 4), data + (ok ? r + e : 0),
+                                   ok ? 16u : 0u);
+                }
+                cp_async_arrive(&m->full[stage]);
+                next_stage();
             }
-            cp_async_arrive(&m->full[l.stage]);
-            if (++l.stage == R) l.stage = 0, l.phase ^= 1;
         }
     }
-}
 
-// 16 codes times their scale -> 16 bf16 in two 16-byte units.
-__device__ __forceinline__ void decode16(uint4 codes, float scale, uint4 &a, uint4 &b)
-{
-    const uint32_t in[4] = {codes.x, codes.y, codes.z, codes.w};
-    uint32_t out[8];
+    // ---- 8-bit rows: loaded to registers some groups ahead, decoded to bf16 on the way to shared memory.
+    static constexpr int kLoads = !FP8 ? 1 : (kVecs < 4 ? kVecs : 4);  // 16-byte loads of a group
+    static constexpr int kGroups = FP8 ? kVecs / kLoads : 1;           // groups of a chunk
+    static constexpr int kAhead = 8 / kLoads;                          // groups in registers
+    struct Codes {
+        uint4 codes[kLoads];
+        float scale[kLoads];
+    };
+
+    __device__ __forceinline__ void rows_codes()
+    {
+        const uint8_t *data = static_cast<const uint8_t *>(k.a.c.data);
+        const float *scales = k.a.c.scales;
+        const int vec = lane & 7, d = k.a.d;
+        const int total = w->n * C * kGroups;
+        Rows next = find(0);
+        const uint8_t *from[kVecs];
+        const float *by[kVecs];
+        int fetched = 0, fg = 0, fc = 0, ft = 0;  // next group to fetch: its number in the chunk, chunk and tile
+        auto fetch = [&](Codes &x) {
+            if (fetched >= total) return;
+            if (fc == 0 && fg == 0) {
+                note(next);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
-            static_cast<__nv_fp8x2_storage_t>((in[i >> 1] >> (16 * (i & 1))) & 0xffffu), __NV_E4M3);
-        const float2 f = __half22float2(__half2(h));
-        out[i] = pack_bf16(f.x * scale, f.y * scale);
+                for (int i = 0; i < kVecs; ++i) {
+                    const int64_t row = __shfl_sync(0xffffffffu, next.row, 4 * i + (lane >> 3));
+                    const int64_t srow = __shfl_sync(0xffffffffu, next.scale, 4 * i + (lane >> 3));
+                    from[i] = row < 0 ? nullptr : data + row + vec * 16;
+                    by[i] = scales + srow;
+                }
+                next = find(ft + 1);
+            }
+            const bool in = fc * 128 + vec * 16 < d;
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                const uint8_t *f = kGroups == 1 || fg == 0 ? from[i] : from[kVecs - kLoads + i];
+                const float *s = kGroups == 1 || fg == 0 ? by[i] : by[kVecs - kLoads + i];
+                x.codes[i] = make_uint4(0u, 0u, 0u, 0u);
+                x.scale[i] = 1.0f;
+                if (in && f) {
+                    x.codes[i] = __ldg(reinterpret_cast<const uint4 *>(f + fc * 128));
+                    x.scale[i] = __ldg(s + fc);
+                }
+            }
+            ++fetched;
+            if (++fg == kGroups) {
+                fg = 0;
+                if (++fc == C) fc = 0, ++ft;
+            }
+        };
+        static_assert(kGroups <= 2, "");
+        const int line0 = lw * kPos + (lane >> 3);
+        const int u = (2 * vec) & 7;
+        const bool odd = vec >= 4;
+        unsigned char *to = smem + (vec >> 2) * F::half_bytes + line0 * 128;
+        int sg = 0;  // group of the chunk being stored
+        auto store = [&](int g, const Codes &x) {
+            if (g >= total) return;
+            if (sg == 0) wait(&m->empty[stage], phase);
+            unsigned char *base = to + stage * F::chunk_bytes + sg * (kLoads * 4 * 128);
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                uint4 a, b;
+                decode16(x.codes[i], x.scale[i], a, b);
+                const int sw = (line0 + 4 * i) & 7;
+                // lanes of the second half store their second unit first: the 8 lanes of a line then
+                // cover all banks in each of the two stores
+                *reinterpret_cast<uint4 *>(base + i * 512 + (((u + odd) ^ sw) << 4)) = odd ? b : a;
+                *reinterpret_cast<uint4 *>(base + i * 512 + (((u + !odd) ^ sw) << 4)) = odd ? a : b;
+            }
+            if (++sg < kGroups) return;
+            sg = 0;
+            fence_proxy_async_shared();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&m->full[stage]);
+            next_stage();
+        };
+        Codes x[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) fetch(x[i]);
+        for (int g = 0; g < total; g += kAhead) {
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                store(g + i, x[i]);
+                fetch(x[i]);
+            }
+        }
     }
-    a = make_uint4(out[0], out[1], out[2], out[3]);
-    b = make_uint4(out[4], out[5], out[6], out[7]);
-}
-
-struct CodeChunk {
-    uint4 codes[4];
-    float scale[4];
 };
 
-template <int C>
-__device__ __forceinline__ void load_fp8(Loader &l, const Waiter &wait, unsigned char *ring)
+// The queries of a unit by two warps; unused columns and elements past d are zeros.
+template <int C, int N>
+__device__ __forceinline__ void load_queries(const Kargs &k, const Unit *w, Misc *m, unsigned char *smem, int warp, int lane)
 {
-    constexpr int R = Cfg<C>::ring;
-    Misc *m = l.m;
-    const uint8_t *data = static_cast<const uint8_t *>(l.k.a.c.data);
-    const float *scales = l.k.a.c.scales;
-    const int vec = l.lane & 7, d = l.k.a.d;
-    const int total = l.w->n * C;
-    Loader::Rows cur{-1, 0}, next = l.find(0);
-    int fetched = 0, fc = 0, ft = 0;  // next chunk to fetch, its column chunk and tile
-    auto fetch = [&](CodeChunk &x) {
-        if (fetched >= total) return;
-        if (fc == 0) {
-            cur = next;
-            l.note(cur);
-            next = l.find(ft + 1);
-        }
-        const bool in = fc * 128 + vec * 16 < d;
+    using F = Cfg<C, N>;
+    const int vec = lane & 15, heads = w->heads, cols = w->cols();
+    const uint32_t to = smem_addr(smem + F::q_off) + (vec >> 3) * F::q_half;
+#pragma unroll 4
+    for (int i = 0; i < N / 4; ++i) {
+        const int col = (i * 2 + warp) * 2 + (lane >> 4);
+        const int row = col / heads;
+        const uint16_t *src = k.a.q + (w->row0 + row) * k.a.q_row_stride +
+                              static_cast<int64_t>(w->head0 + col - row * heads) * k.a.q_head_stride;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int key = 4 * i + (l.lane >> 3);
-            const int64_t row = __shfl_sync(0xffffffffu, cur.row, key);
-            const int64_t srow = __shfl_sync(0xffffffffu, cur.scale, key);
-            x.codes[i] = make_uint4(0u, 0u, 0u, 0u);
-            x.scale[i] = 0.0f;
-            if (in && row >= 0) {
-                x.codes[i] = *reinterpret_cast<const uint4 *>(data + row + fc * 128 + vec * 16);
-                x.scale[i] = scales[srow + fc];
-            }
+        for (int c = 0; c < C; ++c) {
+            const int e = c * 128 + vec * 8;
+            const bool ok = col < cols && e < k.a.d;
+            if (c * 2 + (vec >> 3) < F::q_halves)
+                cp_async16(to + c * 2 * F::q_half + col * 128 + (((vec & 7) ^ (col & 7)) << 4), ok ? src + e : k.a.q,
+                           ok ? 16u : 0u);
         }
-        ++fetched;
-        if (++fc == C) fc = 0, ++ft;
-    };
-    auto store = [&](int g, const CodeChunk &x) {
-        if (g >= total) return;
-        wait(&m->empty[l.stage], l.phase);
-        unsigned char *base = ring + l.stage * kChunkBytes + (vec >> 2) * kHalfBytes;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int line = l.lw * 16 + 4 * i + (l.lane >> 3);
-            uint4 a, b;
-            decode16(x.codes[i], x.scale[i], a, b);
-            const int u = (2 * vec) & 7, sw = line & 7;
-            // lanes of the second half store their second unit first: the 8 lanes of a line then
-            // cover all banks in each of the two stores
-            const bool odd = vec >= 4;
-            *reinterpret_cast<uint4 *>(base + line * 128 + (((u + odd) ^ sw) << 4)) = odd ? b : a;
-            *reinterpret_cast<uint4 *>(base + line * 128 + (((u + !odd) ^ sw) << 4)) = odd ? a : b;
-        }
-        fence_proxy_async_shared();
-        __syncwarp();
-        if (l.lane == 0) mbar_arrive(&m->full[l.stage]);
-        if (++l.stage == R) l.stage = 0, l.phase ^= 1;
-    };
-    CodeChunk x, y;
-    fetch(x);
-    fetch(y);
-    for (int g = 0; g < total; g += 2) {
-        store(g, x);
-        fetch(x);
-        store(g + 1, y);
-        fetch(y);
     }
+    cp_async_wait_all();
+    fence_proxy_async_shared();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&m->q_full);
 }
 
 // ------------------------------------------------------------------------------------ issuing products
-// One warp, all lanes in step (so that descriptors stay in uniform registers), one of them issuing.
-template <int C, bool FP8>
+// One warp, all lanes in step, one of them issuing.
+template <int C, int N, bool FP8>
 struct Issuer {
-    static constexpr int R = Cfg<C>::ring;
+    using F = Cfg<C, N>;
     Misc *m;
     const Waiter &wait;
     // descriptors of the ring's first chunk, of the queries and of P; a step adds its offset / 16
     uint64_t ring_k, ring_v, q0, p0;
     uint32_t o_col, s_col;
-    int vchunks;
+    int halves, vchunks;  // blocks of 64 elements of a row, of 128 of a value
     int s_stage = 0, s_phase = 0, v_stage = 0;
     int s_tile = 0, v_tile = 0;  // tiles issued so far
 
     __device__ __forceinline__ void scores()
     {
-        constexpr uint32_t kScores = umma_idesc(kTile, kCols, false, false);
+        constexpr uint32_t kScores = umma_idesc(F::M, N, false, false);
         const int buf = s_tile & 1;
         wait(&m->s_empty[buf], ((s_tile >> 1) & 1) ^ 1);
-        tmem_fence_after();
+        const uint32_t d = s_col + buf * N;
 #pragma unroll 1
         for (int c = 0; c < C; ++c) {
             wait(&m->full[s_stage], s_phase);
-            if (!FP8) fence_proxy_async_shared();  // the asynchronous copies' arrivals carry no fence of their own
+            if (!FP8) fence_proxy_async_shared();  // (asynchronous copies arrive without a fence of their own)
             tmem_fence_after();
-            const uint64_t a = ring_k + static_cast<uint32_t>(s_stage * (kChunkBytes / 16));
-            const uint64_t b = q0 + static_cast<uint32_t>(c * (2 * kQHalf / 16));
-            const uint32_t d = s_col + buf * kCols;
+            const uint64_t a = ring_k + static_cast<uint32_t>(s_stage * (F::chunk_bytes / 16));
+            const uint64_t b = q0 + static_cast<uint32_t>(c * (2 * F::q_half / 16));
             if (elect_one()) {
                 umma_bf16(d, a, b, kScores, c > 0);
 #pragma unroll
-                for (int s = 1; s < 8; ++s)
-                    umma_bf16(d, a + (s >> 2) * (kHalfBytes / 16) + (s & 3) * 2,
-                              b + (s >> 2) * (kQHalf / 16) + (s & 3) * 2, kScores, true);
+                for (int s = 1; s < 4; ++s) umma_bf16(d, a + s * 2, b + s * 2, kScores, true);
+                if (2 * c + 1 < halves) {
+#pragma unroll
+                    for (int s = 0; s < 4; ++s)
+                        umma_bf16(d, a + F::half_bytes / 16 + s * 2, b + F::q_half / 16 + s * 2, kScores, true);
+                }
             }
-            if (++s_stage == R) s_stage = 0, s_phase ^= 1;
+            __syncwarp();
+            if (++s_stage == F::ring) s_stage = 0, s_phase ^= 1;
         }
         if (elect_one()) umma_commit(&m->s_full[buf]);
         ++s_tile;
@@ -438,24 +526,25 @@ struct Issuer {
 
     __device__ __forceinline__ void values(bool first)
     {
-        constexpr uint32_t kValues = umma_idesc(128, kCols, true, true);
+        constexpr uint32_t kValues = umma_idesc(128, N, true, true);
         const int buf = v_tile & 1;
         wait(&m->p_full[buf], (v_tile >> 1) & 1);
         tmem_fence_after();
-        const uint64_t b = p0 + static_cast<uint32_t>((v_tile % Cfg<C>::pbufs) * (kPBytes / 16));
+        const uint64_t b = p0 + static_cast<uint32_t>((v_tile % F::pbufs) * (F::p_bytes / 16));
 #pragma unroll 1
         for (int c = 0; c < C; ++c) {
-            if (c < vchunks) {
-                const uint64_t a = ring_v + static_cast<uint32_t>(v_stage * (kChunkBytes / 16));
-                const uint32_t d = o_col + c * kCols;
-                if (elect_one()) {
+            const uint64_t a = ring_v + static_cast<uint32_t>(v_stage * (F::chunk_bytes / 16));
+            const uint32_t d = o_col + c * N;
+            if (elect_one()) {
+                if (c < vchunks) {
                     umma_bf16(d, a, b, kValues, !first);
 #pragma unroll
-                    for (int s = 1; s < kTile / 16; ++s) umma_bf16(d, a + s * 128, b + s * 128, kValues, true);
+                    for (int s = 1; s < F::M / 16; ++s) umma_bf16(d, a + s * 128, b + s * 128, kValues, true);
                 }
+                umma_commit(&m->empty[v_stage]);
             }
-            if (elect_one()) umma_commit(&m->empty[v_stage]);
-            if (++v_stage == R) v_stage = 0;
+            __syncwarp();
+            if (++v_stage == F::ring) v_stage = 0;
         }
         if (elect_one()) umma_commit(&m->pv_done[buf]);
         ++v_tile;
@@ -464,254 +553,339 @@ struct Issuer {
     __device__ __forceinline__ void unit(int n, int phase)
     {
         wait(&m->q_full, phase);
-        fence_proxy_async_shared();
         scores();
 #pragma unroll 1
         for (int it = 0; it < n; ++it) {
-            if (Cfg<C>::ahead && it + 1 < n) scores();
+            if (F::ahead && it + 1 < n) scores();
             if (it + 1 == n && elect_one()) umma_commit(&m->q_empty);
             values(it == 0);
-            if (!Cfg<C>::ahead && it + 1 < n) scores();
+            if (!F::ahead && it + 1 < n) scores();
         }
     }
 };
 
 // ------------------------------------------------------------------------------------ softmax
-// Sum (or maximum) over the warp's lanes of each of 32 values a lane holds; lane j gets that of value j.
-template <bool MAX>
-__device__ __forceinline__ float reduce32(float v[32], int lane)
-{
-#pragma unroll
-    for (int s = 16; s > 0; s >>= 1) {
-        const bool up = (lane & s) != 0;
-#pragma unroll
-        for (int j = 0; j < s; ++j) {
-            const float send = up ? v[j] : v[j + s];
-            const float keep = up ? v[j + s] : v[j];
-            const float got = __shfl_xor_sync(0xffffffffu, send, s);
-            v[j] = MAX ? fmaxf(keep, got) : keep + got;
-        }
-    }
-    return v[0];
-}
+// Thread t of warp `quad` of a group holds, of a tile's scores, H blocks of 16 positions by the group's
+// columns in the layout of tmem_ld: 2 H positions by 2 G columns.
+template <int C, int N>
+struct Softmax {
+    using F = Cfg<C, N>;
+    static constexpr int W = F::cols_per_group, G = W / 8, H = F::M / 64;
+    static constexpr int X = 4 * G;  // values of a block of 16 positions
+    const Kargs &k;
+    Misc *m;
+    const Waiter &wait;
+    unsigned char *smem;
+    int group, quad, lane;
+    uint32_t o_tm, s_tm;  // the warp's lanes and the group's columns of the accumulators and scores
+    int tile = 0;         // tiles done so far
+    float ref[2 * G], sum[2 * G];  // of the thread's columns: reference, sum over its positions
 
-template <int C>
-__device__ __forceinline__ void softmax_unit(const Kargs &k, const Unit &w, Misc *m, const Waiter &wait,
-                                             unsigned char *smem, int &tile, int warp, int lane)
-{
-    const int wg = warp >> 2, quad = warp & 3, line = quad * 32 + lane;
-    const int bar = 1 + wg;
-    const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
-    const uint32_t o_tm = m->tmem + lanes + wg * 32, s_tm = m->tmem + lanes + C * kCols + wg * 32;
-    const int vchunks = (k.a.dv + 127) >> 7;
-    const float scale = k.a.scale_log2;
-    const float4 *ref4 = reinterpret_cast<const float4 *>(m->ref + wg * 32);
-    const int *ends = w.end + wg * 32;
-    unsigned char *pbase = smem + Cfg<C>::p_off + line * 128;
-    const int lo = w.lo, n = w.n;
-    float l[32];
-#pragma unroll
-    for (int j = 0; j < 32; ++j) l[j] = 0.0f;
-    if (quad == 0) m->ref[wg * 32 + lane] = -INFINITY;
-    bar_sync(bar, 128);
+    // (a tile of 64 positions lies in lanes 0 .. 15 of each warp's 32)
+    __device__ __forceinline__ int line(int h, int r) const { return quad * (16 * H) + h * 16 + r * 8 + (lane >> 2); }
+    __device__ __forceinline__ int col(int i) const { return group * W + (i >> 1) * 8 + (lane & 3) * 2 + (i & 1); }
 
-    for (int it = 0; it < n; ++it, ++tile) {
-        const int buf = tile & 1;
-        wait(&m->s_full[buf], (tile >> 1) & 1);
-        tmem_fence_after();
-        uint32_t raw[32];
-        tmem_ld32(s_tm + buf * kCols, raw);
+    __device__ __forceinline__ void load_scores(float x[H][X], int buf) const
+    {
+#pragma unroll
+        for (int h = 0; h < H; ++h) tmem_ld<G>(s_tm + buf * N + (static_cast<uint32_t>(h * 16) << 16), x[h]);
         tmem_wait_ld();
-        tmem_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&m->s_empty[buf]);
-        const bool valid = (m->valid[tile & (kValidSlots - 1)][quad] >> lane) & 1u;
-        const int pos = (lo + it) * kTile + line;
-        // a tile some of whose positions are past the end of some, not all, of the CTA's rows
-        const bool edges = !k.a.idx && pos - line + kTile > w.min_end && w.min_end < w.max_end;
-        bool dirty = false;
-        if (edges) {
-            // A position that one row attends to and another does not has weight 0 in the other, but
-            // 0 * NaN is NaN: a row that is not finite is taken out of the values, and the columns that
-            // do attend to it become NaN by their weight.  Such a row makes its score not finite.
-            const bool odd = valid && !(fabsf(__uint_as_float(raw[0])) < INFINITY);
-            if (bar_any(3, kSoftWarps * 32, odd)) {
-                const int stage0 = static_cast<int>((static_cast<int64_t>(tile) * C) % Cfg<C>::ring);
-                auto unit16 = [&](int e) {
-                    return smem + ((stage0 + (e >> 7)) % Cfg<C>::ring) * kChunkBytes + ((e >> 6) & 1) * kHalfBytes +
-                           line * 128 + ((((e >> 3) & 7) ^ (line & 7)) << 4);
-                };
-                if (odd)
-                    for (int e = 0; e < k.a.dv; ++e)
-                        dirty |= (reinterpret_cast<const uint16_t *>(unit16(e))[e & 7] & 0x7f80u) == 0x7f80u;
-                bar_sync(3, kSoftWarps * 32);
-                if (dirty && wg == 0)
-                    for (int e = 0; e < k.a.dv; e += 8)
-                        *reinterpret_cast<uint4 *>(unit16(e)) = make_uint4(0u, 0u, 0u, 0u);
-            }
-        }
-        // x = log2 of the weight before the column's reference is taken off, -inf where masked
-        const bool whole = __all_sync(0xffffffffu, valid) && !edges;
-        auto masked = [&](float x, int j) { return valid && !(edges && pos >= ends[j]) ? x : -INFINITY; };
-        float x[32];
-#pragma unroll
-        for (int j4 = 0; j4 < 8; ++j4) {
-            const float4 r = ref4[j4];
-            x[4 * j4] = fmaf(__uint_as_float(raw[4 * j4]), scale, -r.x);
-            x[4 * j4 + 1] = fmaf(__uint_as_float(raw[4 * j4 + 1]), scale, -r.y);
-            x[4 * j4 + 2] = fmaf(__uint_as_float(raw[4 * j4 + 2]), scale, -r.z);
-            x[4 * j4 + 3] = fmaf(__uint_as_float(raw[4 * j4 + 3]), scale, -r.w);
-        }
-        if (!whole) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) x[j] = masked(x[j], j);
-        }
-        float top = x[0];
-#pragma unroll
-        for (int j = 1; j < 32; ++j) top = fmaxf(top, x[j]);
-        // (a column without positions yet has the reference -inf, which any score exceeds)
-        if (bar_any(bar, 128, top > kRefSlack)) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) x[j] = masked(__uint_as_float(raw[j]) * scale, j);
-            m->wmax[quad][wg * 32 + lane] = reduce32<true>(x, lane);
-            bar_sync(bar, 128);
-            if (quad == 0) {
-                const int c = wg * 32 + lane;
-                const float old = m->ref[c];
-                const float now = fmaxf(fmaxf(old, fmaxf(m->wmax[0][c], m->wmax[1][c])), fmaxf(m->wmax[2][c], m->wmax[3][c]));
-                m->factor[c] = old == now ? 1.0f : exp2_approx(old - now);
-                m->ref[c] = now;
-            }
-            bar_sync(bar, 128);
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-                const float r = m->ref[wg * 32 + j];
-                x[j] = masked(fmaf(__uint_as_float(raw[j]), scale, r == -INFINITY ? 0.0f : -r), j);
-                l[j] *= m->factor[wg * 32 + j];
-            }
-            if (it > 0) {
-                wait(&m->pv_done[(tile - 1) & 1], ((tile - 1) >> 1) & 1);
-                tmem_fence_after();
-                for (int c = 0; c < vchunks; ++c) {
-                    tmem_ld32(o_tm + c * kCols, raw);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        raw[j] = __float_as_uint(__uint_as_float(raw[j]) * m->factor[wg * 32 + j]);
-                    tmem_st32(o_tm + c * kCols, raw);
-                }
-                tmem_wait_st();
-            }
-        }
-        if (dirty) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-                if (pos < ends[j]) x[j] = __int_as_float(0x7fffffff);
-        }
-        // the buffer of P is free once the product that read it is done
-        if (tile >= Cfg<C>::pbufs) {
-            const int before = tile - Cfg<C>::pbufs;
-            wait(&m->pv_done[before & 1], (before >> 1) & 1);
-        }
-        unsigned char *prow = pbase + (tile % Cfg<C>::pbufs) * kPBytes;
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            uint32_t out[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int j = u * 8 + i * 2;
-                const float p0 = exp2_approx(x[j]), p1 = exp2_approx(x[j + 1]);
-                l[j] += p0;
-                l[j + 1] += p1;
-                out[i] = pack_bf16(p0, p1);
-            }
-            *reinterpret_cast<uint4 *>(prow + (((wg * 4 + u) ^ (line & 7)) << 4)) =
-                make_uint4(out[0], out[1], out[2], out[3]);
-        }
-        fence_proxy_async_shared();
-        tmem_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&m->p_full[buf]);
     }
 
-    // column sums, in a fixed order
-    m->lsum[quad][wg * 32 + lane] = reduce32<false>(l, lane);
-    bar_sync(bar, 128);
-    const int col = wg * 32 + lane, cols = w.cols();
-    const float sum = (m->lsum[0][col] + m->lsum[1][col]) + (m->lsum[2][col] + m->lsum[3][col]);
-    const int64_t out_row = (w.row0 + col / w.heads) * k.a.h + w.head0 + col % w.heads;  // of lane's column
-    if (quad == 0) {
-        m->inv[col] = sum == 0.0f ? 0.0f : 1.0f / sum;
-        if (col < cols) {
-            if (k.p.parts > 1)
-                k.part_ml[out_row * k.p.parts + w.part] = make_float2(m->ref[col], sum);
-            else if (k.a.lse)
-                k.a.lse[out_row] = sum == 0.0f ? -INFINITY : (m->ref[col] + log2f(sum)) * 0.69314718055994531f;
+    // What the thread's positions and columns of a tile are masked by.
+    struct Mask {
+        bool edges;        // some positions are past the end of some, not all, of the CTA's rows
+        uint32_t valid;    // bit 2 h + r: the position has a cache row
+        int pos0;          // position of line 0
+        const int *ends;
+    };
+    __device__ __forceinline__ float masked(const Mask &a, float v, int h, int i) const
+    {
+        const int r = (i >> 1) & 1, c = ((i >> 2) << 1) | (i & 1);
+        const bool in = ((a.valid >> (2 * h + r)) & 1u) && !(a.edges && a.pos0 + line(h, r) >= a.ends[col(c)]);
+        return in ? v : -INFINITY;
+    }
+
+    // Scores exceed their columns' references by too much (or a column has none yet): new references, sums
+    // and accumulators brought to them, x formed again.
+    __device__ __forceinline__ void move_references(float x[H][X], int buf, bool started, const Mask &mask)
+    {
+        float factor[2 * G];
+        load_scores(x, buf);
+#pragma unroll
+        for (int c = 0; c < 2 * G; ++c) {
+            float top = -INFINITY;
+#pragma unroll
+            for (int h = 0; h < H; ++h)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const int i = (c >> 1) * 4 + r * 2 + (c & 1);
+                    top = fmaxf(top, masked(mask, x[h][i] * k.a.scale_log2, h, i));
+                }
+#pragma unroll
+            for (int s = 4; s < 32; s <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+            if (lane < 4) m->part[quad][col(c)] = top;
+        }
+        bar_sync(1 + group, 128);
+#pragma unroll
+        for (int c = 0; c < 2 * G; ++c) {
+            const int at = col(c);
+            const float now = fmaxf(fmaxf(ref[c], fmaxf(m->part[0][at], m->part[1][at])),
+                                    fmaxf(m->part[2][at], m->part[3][at]));
+            factor[c] = ref[c] == now ? 1.0f : exp2_approx(ref[c] - now);
+            ref[c] = now;
+            sum[c] *= factor[c];
+        }
+        if (started) {
+            wait(&m->pv_done[(tile - 1) & 1], ((tile - 1) >> 1) & 1);
+            tmem_fence_after();
+            const int vchunks = (k.a.dv + 127) >> 7;
+            for (int c = 0; c < 2 * vchunks; ++c) {
+                const uint32_t at = o_tm + (c >> 1) * N + (static_cast<uint32_t>((c & 1) * 16) << 16);
+                float o[X];
+                tmem_ld<G>(at, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < X; ++i) o[i] *= factor[((i >> 2) << 1) | (i & 1)];
+                tmem_st<G>(at, o);
+            }
+            tmem_wait_st();
+        }
+        subtract(x, mask, true);
+    }
+
+    // x = score * scale - reference: log2 of the weight, -inf where masked.
+    __device__ __forceinline__ void subtract(float x[H][X], const Mask &mask, bool apply) const
+    {
+#pragma unroll
+        for (int h = 0; h < H; ++h)
+#pragma unroll
+            for (int i = 0; i < X; ++i) {
+                const float r = ref[((i >> 2) << 1) | (i & 1)];
+                x[h][i] = fmaf(x[h][i], k.a.scale_log2, -r);
+                if (apply) x[h][i] = masked(mask, x[h][i], h, i);
+            }
+    }
+
+    // A position that one row attends to and another does not has weight 0 in the other, but 0 * NaN is
+    // NaN: a cache row that is not finite is taken out of the values here (its bit 2 h + r is returned), and
+    // the columns that do attend to it become NaN by their weight.  Such a row makes its scores not finite.
+    __device__ __forceinline__ uint32_t take_out(const float x[H][X], const Mask &mask) const
+    {
+        uint32_t dirty = 0;
+#pragma unroll
+        for (int h = 0; h < H; ++h)
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+                if (((mask.valid >> (2 * h + r)) & 1u) && !(fabsf(x[h][2 * r]) < INFINITY)) dirty |= 1u << (2 * h + r);
+        if (!bar_any(5, kSoftWarps * 32, dirty != 0)) return 0;
+        const int stage0 = static_cast<int>((static_cast<int64_t>(tile) * C) % F::ring);
+        auto unit16 = [&](int at, int e) {
+            return smem + ((stage0 + (e >> 7)) % F::ring) * F::chunk_bytes + ((e >> 6) & 1) * F::half_bytes + at * 128 +
+                   ((((e >> 3) & 7) ^ (at & 7)) << 4);
+        };
+        for (int b = 0; b < 2 * H; ++b) {
+            if (!((dirty >> b) & 1u)) continue;
+            bool bad = false;
+            for (int e = 0; e < k.a.dv; ++e)
+                bad |= (reinterpret_cast<const uint16_t *>(unit16(line(b >> 1, b & 1), e))[e & 7] & 0x7f80u) == 0x7f80u;
+            if (!bad) dirty &= ~(1u << b);
+        }
+        bar_sync(5, kSoftWarps * 32);
+        for (int b = 0; b < 2 * H; ++b)
+            if (((dirty >> b) & 1u) && group == 0 && (lane & 3) == 0)
+                for (int e = 0; e < k.a.dv; e += 8)
+                    *reinterpret_cast<uint4 *>(unit16(line(b >> 1, b & 1), e)) = make_uint4(0u, 0u, 0u, 0u);
+        return dirty;
+    }
+
+    __device__ __forceinline__ void tiles(const Unit &w)
+    {
+        const int n = w.n;
+        const uint32_t vshift = line(0, 0) & 31;  // the thread's first position within its word of validity bits
+        for (int it = 0; it < n; ++it, ++tile) {
+            const int buf = tile & 1;
+            Mask mask;
+            mask.pos0 = (w.lo + it) * F::M;
+            mask.ends = w.end;
+            mask.edges = !k.a.idx && mask.pos0 + F::M > w.min_end && w.min_end < w.max_end;
+            wait(&m->s_full[buf], (tile >> 1) & 1);
+            tmem_fence_after();
+            const uint32_t word = m->valid[tile & (kValidSlots - 1)][line(0, 0) >> 5];
+            float x[H][X];
+            load_scores(x, buf);
+            mask.valid = 0;
+#pragma unroll
+            for (int b = 0; b < 2 * H; ++b) mask.valid |= ((word >> (vshift + 8 * b)) & 1u) << b;
+            const uint32_t dirty = mask.edges ? take_out(x, mask) : 0u;
+            const bool whole = __all_sync(0xffffffffu, mask.valid == (1u << (2 * H)) - 1u) && !mask.edges;
+            subtract(x, mask, false);
+            if (!whole) {
+#pragma unroll
+                for (int h = 0; h < H; ++h)
+#pragma unroll
+                    for (int i = 0; i < X; ++i) x[h][i] = masked(mask, x[h][i], h, i);
+            }
+            float top = x[0][0];
+#pragma unroll
+            for (int h = 0; h < H; ++h)
+#pragma unroll
+                for (int i = 0; i < X; ++i) top = fmaxf(top, x[h][i]);
+            // (a column without positions yet has the reference -inf, which any score exceeds)
+            if (bar_any(1 + group, 128, top > kRefSlack)) move_references(x, buf, it > 0, mask);
+            tmem_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&m->s_empty[buf]);
+            if (dirty) {
+#pragma unroll
+                for (int h = 0; h < H; ++h)
+#pragma unroll
+                    for (int i = 0; i < X; ++i)
+                        if (((dirty >> (2 * h + ((i >> 1) & 1))) & 1u) && x[h][i] != -INFINITY)
+                            x[h][i] = __int_as_float(0x7fffffff);
+            }
+            // the buffer of P is free once the product that read it is done
+            if (tile >= F::pbufs) {
+                const int before = tile - F::pbufs;
+                wait(&m->pv_done[before & 1], (before >> 1) & 1);
+            }
+            unsigned char *p = smem + F::p_off + (tile % F::pbufs) * F::p_bytes + (group * W / 64) * F::p_block +
+                               (lane & 3) * 4;
+#pragma unroll
+            for (int h = 0; h < H; ++h)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const int at = line(h, r);
+#pragma unroll
+                    for (int g = 0; g < G; ++g) {
+                        const float p0 = exp2_approx(x[h][4 * g + 2 * r]), p1 = exp2_approx(x[h][4 * g + 2 * r + 1]);
+                        sum[2 * g] += p0;
+                        sum[2 * g + 1] += p1;
+                        const int unit = (group * W % 64) / 8 + g;
+                        *reinterpret_cast<uint32_t *>(p + at * 128 + ((unit ^ (at & 7)) << 4)) = pack_bf16(p0, p1);
+                    }
+                }
+            fence_proxy_async_shared();
+            tmem_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&m->p_full[buf]);
         }
     }
-    bar_sync(bar, 128);
-    if (n > 0) {
-        wait(&m->pv_done[(tile - 1) & 1], ((tile - 1) >> 1) & 1);
-        tmem_fence_after();
-    }
-    if (k.p.parts > 1) {
-        // (a part without positions has the sum 0: its accumulators are not read)
-        for (int c = 0; n > 0 && c < vchunks; ++c) {
-            uint32_t o[32];
-            tmem_ld32(o_tm + c * kCols, o);
-            tmem_wait_ld();
-            const int e = c * 128 + line;
+
+    __device__ __forceinline__ void unit(const Unit &w)
+    {
+        const int bar = 1 + group, cols = w.cols(), n = w.n;
+        auto out_row = [&](int c) { return static_cast<int64_t>(w.out[c]); };
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-                const int64_t r = __shfl_sync(0xffffffffu, out_row, j);
-                if (wg * 32 + j < cols && e < k.a.dv)
-                    k.part_o[(r * k.p.parts + w.part) * k.a.dv + e] = __uint_as_float(o[j]);
+        for (int c = 0; c < 2 * G; ++c) {
+            ref[c] = -INFINITY;
+            sum[c] = 0.0f;
+        }
+        tiles(w);
+        // column sums, in a fixed order
+        bar_sync(bar, 128);
+#pragma unroll
+        for (int c = 0; c < 2 * G; ++c) {
+#pragma unroll
+            for (int s = 4; s < 32; s <<= 1) sum[c] += __shfl_xor_sync(0xffffffffu, sum[c], s);
+            if (lane < 4) m->part[quad][col(c)] = sum[c];
+        }
+        bar_sync(bar, 128);
+        if (quad == 0 && lane < 4) {
+#pragma unroll
+            for (int c = 0; c < 2 * G; ++c) {
+                const int at = col(c);
+                const float l = (m->part[0][at] + m->part[1][at]) + (m->part[2][at] + m->part[3][at]);
+                m->inv[at] = l == 0.0f ? 0.0f : 1.0f / l;
+                if (at < cols) {
+                    if (k.p.parts > 1)
+                        k.part_ml[out_row(at) * k.p.parts + w.part] = make_float2(ref[c], l);
+                    else if (k.a.lse)
+                        k.a.lse[out_row(at)] = l == 0.0f ? -INFINITY : (ref[c] + log2f(l)) * 0.69314718055994531f;
+                }
             }
         }
-        return;
-    }
-    // the group's 32 columns x 128 elements through its half of a P buffer (free by now), so that whole
-    // 16-byte vectors of a column are written
-    unsigned char *stage = smem + Cfg<C>::p_off + wg * (kPBytes / 2);
-    for (int c = 0; c < vchunks; ++c) {
-        uint32_t o[32];
+        bar_sync(bar, 128);
         if (n > 0) {
-            tmem_ld32(o_tm + c * kCols, o);
-            tmem_wait_ld();
-        } else {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) o[j] = 0u;
+            wait(&m->pv_done[(tile - 1) & 1], ((tile - 1) >> 1) & 1);
+            tmem_fence_after();
         }
+        const int vchunks = (k.a.dv + 127) >> 7;
+        if (k.p.parts > 1) {
+            // (a part without positions has the sum 0: its accumulators are not read)
+            for (int b = 0; n > 0 && b < 2 * vchunks; ++b) {
+                float o[X];
+                tmem_ld<G>(o_tm + (b >> 1) * N + (static_cast<uint32_t>((b & 1) * 16) << 16), o);
+                tmem_wait_ld();
+                const int e = (b >> 1) * 128 + quad * 32 + (b & 1) * 16 + (lane >> 2);
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-            const float v = __uint_as_float(o[j]) * m->inv[wg * 32 + j];
-            *reinterpret_cast<__nv_bfloat16 *>(stage + j * 256 + line * 2) = __float2bfloat16_rn(v);
+                for (int c = 0; c < 2 * G; ++c) {
+                    const int at = col(c);
+                    if (at >= cols) continue;
+                    float *to = k.part_o + (out_row(at) * k.p.parts + w.part) * k.a.dv + e;
+                    if (e < k.a.dv) to[0] = o[(c >> 1) * 4 + (c & 1)];
+                    if (e + 8 < k.a.dv) to[8] = o[(c >> 1) * 4 + 2 + (c & 1)];
+                }
+            }
+            return;
         }
-        bar_sync(bar, 128);
+        // the group's columns x 128 elements through its quarter of a P buffer pair (free by now), so that
+        // whole 16-byte vectors of a column are written; unit u of column j lies at unit u ^ (j mod 16)
+        unsigned char *stage = smem + F::p_off + group * (W * 256);
+        float inv[2 * G];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int j = quad * 8 + i * 2 + (lane >> 4), e = c * 128 + (lane & 15) * 8;
-            const int64_t r = __shfl_sync(0xffffffffu, out_row, j);
-            if (wg * 32 + j < cols && e < k.a.dv)
-                __stcs(reinterpret_cast<uint4 *>(k.a.out + r * k.a.dv + e),
-                       *reinterpret_cast<const uint4 *>(stage + j * 256 + (lane & 15) * 16));
+        for (int c = 0; c < 2 * G; ++c) inv[c] = m->inv[col(c)];
+        uint16_t *to[W / 8];  // the vectors this thread writes: column, element 8 (lane mod 16); null: unused
+#pragma unroll
+        for (int i = 0; i < W / 8; ++i) {
+            const int at = group * W + quad * (W / 4) + i * 2 + (lane >> 4);
+            to[i] = at < cols ? k.a.out + out_row(at) * k.a.dv + (lane & 15) * 8 : nullptr;
         }
-        bar_sync(bar, 128);
+        for (int ch = 0; ch < vchunks; ++ch) {
+            float o[2][X];
+            if (n > 0) {
+                tmem_ld<G>(o_tm + ch * N, o[0]);
+                tmem_ld<G>(o_tm + ch * N + (16u << 16), o[1]);
+                tmem_wait_ld();
+            } else {
+#pragma unroll
+                for (int i = 0; i < 2 * X; ++i) o[i / X][i % X] = 0.0f;
+            }
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int i = 0; i < X; ++i) {
+                    const int c = ((i >> 2) << 1) | (i & 1), j = col(c) - group * W;
+                    const int e = quad * 32 + b * 16 + ((i >> 1) & 1) * 8 + (lane >> 2);
+                    *reinterpret_cast<__nv_bfloat16 *>(stage + j * 256 + (((e >> 3) ^ (j & 15)) << 4) + (e & 7) * 2) =
+                        __float2bfloat16_rn(o[b][i] * inv[c]);
+                }
+            bar_sync(bar, 128);
+#pragma unroll
+            for (int i = 0; i < W / 8; ++i) {
+                const int j = quad * (W / 4) + i * 2 + (lane >> 4), u = lane & 15;
+                if (to[i] && ch * 128 + u * 8 < k.a.dv)
+                    __stcs(reinterpret_cast<uint4 *>(to[i] + ch * 128),
+                           *reinterpret_cast<const uint4 *>(stage + j * 256 + ((u ^ (j & 15)) << 4)));
+            }
+            bar_sync(bar, 128);
+        }
+        bar_sync(5, kSoftWarps * 32);  // the next unit's P covers every group's staging
     }
-    bar_sync(3, kSoftWarps * 32);  // the next unit's P covers both groups' staging
-}
+};
 
 // ------------------------------------------------------------------------------------ the kernel
-template <int C, bool FP8>
-__global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_constant__ Kargs k)
+template <int C, int N, bool FP8>
+__global__ void __launch_bounds__(Cfg<C, N>::threads, 1) attention_kernel(const __grid_constant__ Kargs k)
 {
+    using F = Cfg<C, N>;
     extern __shared__ __align__(1024) unsigned char smem[];
-    Misc *m = reinterpret_cast<Misc *>(smem + Cfg<C>::misc_off);
+    Misc *m = reinterpret_cast<Misc *>(smem + F::misc_off);
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
     const int64_t units = k.p.items * k.p.parts;
     if (t == 0) {
-        for (int i = 0; i < Cfg<C>::ring; ++i) {
-            mbar_init(&m->full[i], FP8 ? kLoadWarps : kLoadWarps * 32);
+        for (int i = 0; i < F::ring; ++i) {
+            mbar_init(&m->full[i], FP8 ? F::load_warps : F::load_warps * 32);
             mbar_init(&m->empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -720,9 +894,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
             mbar_init(&m->p_full[i], kSoftWarps);
             mbar_init(&m->pv_done[i], 1);
             mbar_init(&m->unit_full[i], 1);
-            mbar_init(&m->unit_empty[i], kSoftWarps + 1 + kLoadWarps);
+            mbar_init(&m->unit_empty[i], kSoftWarps + 3 + F::load_warps);
         }
-        mbar_init(&m->q_full, kLoadWarps * 32);
+        mbar_init(&m->q_full, 2);
         mbar_init(&m->q_empty, 1);
         fence_mbar_init();
         m->abort = 0;
@@ -743,23 +917,27 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     };
 
     if (warp < kSoftWarps) {
-        regs_up<kSoftRegs>();
-        int tile = 0, i = 0;
+        regs_to<F::soft_regs, (F::soft_regs > F::launch_regs)>();
+        const int group = warp >> 2, quad = warp & 3;
+        const uint32_t at = m->tmem + (static_cast<uint32_t>(quad * 32) << 16) + group * F::cols_per_group;
+        Softmax<C, N> soft{k, m, wait, smem, group, quad, lane, at, at + C * N};
+        int i = 0;
         for (int64_t u = blockIdx.x; u < units; u += gridDim.x, ++i) {
-            softmax_unit<C>(k, *take(i), m, wait, smem, tile, warp, lane);
+            soft.unit(*take(i));
             give(i);
         }
     } else if (warp < kLoadWarp0) {
-        regs_down<kMmaRegs>();
+        regs_to<F::mma_regs, false>();
         if (warp == kMmaWarp) {
-            Issuer<C, FP8> issue{m, wait};
+            Issuer<C, N, FP8> issue{m, wait};
             issue.ring_k = umma_desc(smem_addr(smem), 16, 1024);
-            issue.ring_v = umma_desc(smem_addr(smem), kHalfBytes, 1024);
-            issue.q0 = umma_desc(smem_addr(smem + Cfg<C>::q_off), 16, 1024);
-            issue.p0 = umma_desc(smem_addr(smem + Cfg<C>::p_off), kHalfBytes, 1024);
+            issue.ring_v = umma_desc(smem_addr(smem), F::half_bytes, 1024);
+            issue.q0 = umma_desc(smem_addr(smem + F::q_off), 16, 1024);
+            issue.p0 = umma_desc(smem_addr(smem + F::p_off), F::p_block, 1024);
             const uint32_t tm = __reduce_max_sync(0xffffffffu, m->tmem);  // (uniform)
             issue.o_col = tm;
-            issue.s_col = tm + C * kCols;
+            issue.s_col = tm + C * N;
+            issue.halves = (k.a.d + 63) >> 6;
             issue.vchunks = (k.a.dv + 127) >> 7;
             int i = 0, loaded = 0;
             for (int64_t u = blockIdx.x; u < units; u += gridDim.x, ++i) {
@@ -771,24 +949,32 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
             int i = 0;
             for (int64_t u = blockIdx.x; u < units; u += gridDim.x, ++i) {
                 wait(&m->unit_empty[i & 1], ((i >> 1) & 1) ^ 1);
-                make_unit(k, u, &m->unit[i & 1], lane);
+                make_unit<N, F::M>(k, u, &m->unit[i & 1], lane);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&m->unit_full[i & 1]);
             }
+        } else {
+            int i = 0, loaded = 0;
+            for (int64_t u = blockIdx.x; u < units; u += gridDim.x, ++i) {
+                const Unit *w = take(i);
+                if (w->n > 0) {
+                    wait(&m->q_empty, (loaded++ & 1) ^ 1);
+                    load_queries<C, N>(k, w, m, smem, warp - kUnitWarp - 1, lane);
+                }
+                give(i);
+            }
         }
     } else {
-        regs_down<kLoadRegs>();
-        Loader l{k, m, nullptr, k.a.t.max_pages * k.a.c.page_size, lane, warp - kLoadWarp0, 0, 1, 0};
-        int i = 0, loaded = 0;
+        regs_to<F::load_regs, true>();
+        Loader<C, N, FP8> load{k, m, wait, smem, lane, warp - kLoadWarp0};
+        int i = 0;
         for (int64_t u = blockIdx.x; u < units; u += gridDim.x, ++i) {
-            l.w = take(i);
-            if (l.w->n > 0) {
-                wait(&m->q_empty, (loaded++ & 1) ^ 1);
-                l.queries<C>(smem + Cfg<C>::q_off);
+            load.w = take(i);
+            if (load.w->n > 0) {
                 if (FP8)
-                    load_fp8<C>(l, wait, smem);
+                    load.rows_codes();
                 else
-                    load_bf16<C>(l, wait, smem);
+                    load.rows_bf16();
             }
             give(i);
         }
@@ -830,33 +1016,44 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Kargs
     if (threadIdx.x == 0 && k.a.lse) k.a.lse[item] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
 }
 
-template <int C, bool FP8>
+template <int C, int N, bool FP8>
 cudaError_t launch(const Kargs &k, cudaStream_t s)
 {
-    constexpr size_t smem = Cfg<C>::misc_off + sizeof(Misc);
+    using F = Cfg<C, N>;
+    constexpr size_t smem = F::misc_off + sizeof(Misc);
     static_assert(smem <= 232448, "more than a CTA may use");
     static_assert(smem > 116 * 1024, "one CTA an SM: each takes all of the tensor memory");
-    cudaError_t e = cudaFuncSetAttribute(attention_kernel<C, FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    static_assert(4 * F::cols_per_group * 256 <= F::pbufs * F::p_bytes, "outputs are staged where P was");
+    cudaError_t e = cudaFuncSetAttribute(attention_kernel<C, N, FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(smem));
     if (e != cudaSuccess) return e;
     const int64_t units = k.p.items * k.p.parts, sms = device_sm_count();
-    attention_kernel<C, FP8><<<static_cast<unsigned>(units < sms ? units : sms), kThreads, smem, s>>>(k);
+    attention_kernel<C, N, FP8><<<static_cast<unsigned>(units < sms ? units : sms), F::threads, smem, s>>>(k);
     return cudaGetLastError();
 }
 
-Plan plan_of(int64_t rows, int64_t h, int64_t b, int64_t positions, bool idx_given)
+template <int C, int N>
+cudaError_t launch(const Kargs &k, cudaStream_t s)
+{
+    return k.a.c.scales ? launch<C, N, true>(k, s) : launch<C, N, false>(k, s);
+}
+
+Plan plan_of(int64_t rows, int64_t h, int64_t d, int64_t b, int64_t positions, bool idx_given)
 {
     Plan p{};
     const int64_t per = rows / b;
-    p.heads_per_tile = static_cast<int>(h < kCols ? h : kCols);
-    p.head_blocks = static_cast<int>((h + kCols - 1) / kCols);
+    // 128 columns where the kernel has them and rows and heads fill more than 64
+    const int64_t cols = d <= 192 && (idx_given ? h : h * per) > 64 ? 128 : 64;
+    p.cols = static_cast<int>(cols);
+    p.heads_per_tile = static_cast<int>(h < cols ? h : cols);
+    p.head_blocks = static_cast<int>((h + cols - 1) / cols);
     // rows that share a tile share its positions; a row with a list has its own
-    const int64_t fit = idx_given ? 1 : kCols / p.heads_per_tile;
+    const int64_t fit = idx_given ? 1 : cols / p.heads_per_tile;
     p.rows_per_tile = static_cast<int>(fit < per ? fit : per);
     p.tiles_per_seq = (per + p.rows_per_tile - 1) / p.rows_per_tile;
     p.items = b * p.tiles_per_seq * p.head_blocks;
     // parts: as many as keep the fewest tiles in a row, counting a part's start and end as 1.5 tiles
-    const int64_t tiles = (positions + kTile - 1) / kTile;
+    const int64_t tiles = (positions + 127) / 128;
     const int64_t sms = device_sm_count() > 0 ? device_sm_count() : 1;
     p.parts = 1;
     double best = 0.0;
@@ -876,10 +1073,10 @@ size_t part_bytes(int64_t items, int parts) { return static_cast<size_t>((items 
 
 }  // namespace
 
-size_t cache_attention_workspace(int64_t rows, int64_t h, int64_t, int64_t dv, int64_t b, int64_t positions,
+size_t cache_attention_workspace(int64_t rows, int64_t h, int64_t d, int64_t dv, int64_t b, int64_t positions,
                                  bool idx_given)
 {
-    const Plan p = plan_of(rows, h, b, positions, idx_given);
+    const Plan p = plan_of(rows, h, d, b, positions, idx_given);
     if (p.parts == 1) return 0;
     return part_bytes(rows * h, p.parts) + static_cast<size_t>(rows * h) * p.parts * dv * 4;
 }
@@ -888,19 +1085,18 @@ cudaError_t launch_cache_attention(const CacheAttnArgs &a, cudaStream_t s)
 {
     Kargs k{};
     k.a = a;
-    k.p = plan_of(a.rows, a.h, a.rows / a.t.rows_per_seq, a.idx ? a.n : a.t.max_pages * a.c.page_size, a.idx != nullptr);
+    k.p = plan_of(a.rows, a.h, a.d, a.rows / a.t.rows_per_seq, a.idx ? a.n : a.t.max_pages * a.c.page_size, a.idx != nullptr);
     if (k.p.parts > 1) {
         k.part_ml = static_cast<float2 *>(a.ws);
         k.part_o = reinterpret_cast<float *>(static_cast<unsigned char *>(a.ws) + part_bytes(a.rows * a.h, k.p.parts));
     }
-    const bool fp8 = a.c.scales != nullptr;
     cudaError_t e;
-    switch ((a.d + 127) / 128) {
-    case 1: e = fp8 ? launch<1, true>(k, s) : launch<1, false>(k, s); break;
-    case 2: e = fp8 ? launch<2, true>(k, s) : launch<2, false>(k, s); break;
-    case 3: e = fp8 ? launch<3, true>(k, s) : launch<3, false>(k, s); break;
-    default: e = fp8 ? launch<4, true>(k, s) : launch<4, false>(k, s); break;
-    }
+    if (k.p.cols == 128)
+        e = a.d <= 128 ? launch<1, 128>(k, s) : launch<2, 128>(k, s);
+    else if (a.d <= 256)
+        e = a.d <= 128 ? launch<1, 64>(k, s) : launch<2, 64>(k, s);
+    else
+        e = a.d <= 384 ? launch<3, 64>(k, s) : launch<4, 64>(k, s);
     if (e != cudaSuccess || k.p.parts == 1) return e;
     join_kernel<<<static_cast<unsigned>(a.rows * a.h), 128, 0, s>>>(k);
     return cudaGetLastError();
