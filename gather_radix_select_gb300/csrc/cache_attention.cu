@@ -10,7 +10,7 @@
 // once and used for both products.
 //
 // The sum of exponentials needs no maximum, only a reference that keeps exp2 in range.  `ref` is the
-// column's largest score when it was last set; while no score exceeds it by more than 2^8 the tile is
+// column's largest score when it was last set; while no weight exceeds it by more than 2^24 the tile is
 // taken with one vote.  Else the columns' maxima are formed across the positions and the sums and
 // accumulators are rescaled.  Sums are kept per thread (its positions) and joined at the end.
 //
@@ -42,7 +42,9 @@ constexpr int kLoadWarp0 = kSoftWarps + 4;
 constexpr int kMaxRing = 5;
 constexpr int kValidSlots = 16;            // tiles whose validity bits are kept (more than the ring holds)
 constexpr int kMaxSplit = 64;
-constexpr float kRefSlack = 8.0f;          // log2: how far a score may exceed its column's reference
+// log2 of how far a weight may exceed 1 before its column's reference moves.  bf16 has the range of fp32, so
+// the weights lose nothing by it; products stay finite for values up to 2^100.
+constexpr float kRefSlack = 24.0f;
 constexpr long long kWaitCycles = 4000000000LL;  // about 2 s
 constexpr uint32_t kSuspend = 1000;
 constexpr int32_t kTimeout = 5;            // SEL_ETIMEOUT
@@ -52,7 +54,7 @@ constexpr int32_t kTimeout = 5;            // SEL_ETIMEOUT
 // So 128 columns are taken where queries, P and two tiles of rows fit beside one another: rows of up to 192
 // elements.  (64-position tiles, two of which fit for rows of 512 elements, take 45.4 for 64 x 64 x 16, and
 // were measured slower: 716 against 532 us for 4096 rows of 64 heads over 512 selected positions.)
-template <int C, int N>
+template <int C, int N, bool FP8>
 struct Cfg {
     static_assert(N == 64 || N == 128, "");
     static constexpr bool wide = N == 128;
@@ -70,14 +72,13 @@ struct Cfg {
     static constexpr int p_off = q_off + q_halves * q_half;
     static constexpr int misc_off = p_off + pbufs * p_bytes;
     static constexpr int cols_per_group = N / 4;
-    static constexpr int load_warps = wide ? 4 : 8;
+    static constexpr int load_warps = wide && FP8 ? 4 : 8;
     static constexpr int threads = (kLoadWarp0 + load_warps) * 32;
-    // Registers a thread after the roles part, of 896 x 72 (768 x 80) at the launch:
-    // 512 x 64 + 128 x 40 + 256 x 96 = 62464 <= 64512;  512 x 88 + 128 x 40 + 128 x 88 = 61440.
-    static constexpr int launch_regs = wide ? 80 : 72;
+    // Registers a thread after the roles part, of 896 x 72 (768 x 80) at the launch.
+    static constexpr int launch_regs = load_warps == 4 ? 80 : 72;
     static constexpr int soft_regs = wide ? 88 : 64;
     static constexpr int mma_regs = 40;
-    static constexpr int load_regs = wide ? 88 : 96;
+    static constexpr int load_regs = load_warps == 4 ? 88 : (wide ? 48 : 96);
     static_assert(ring >= C && ring <= kMaxRing, "");
     static_assert(512 * soft_regs + 128 * mma_regs + 32 * load_warps * load_regs <= threads * launch_regs, "");
 };
@@ -264,7 +265,7 @@ __device__ __forceinline__ void decode16(uint4 codes, float scale, uint4 &a, uin
 
 template <int C, int N, bool FP8>
 struct Loader {
-    using F = Cfg<C, N>;
+    using F = Cfg<C, N, FP8>;
     // Warp lw stages positions lw * kPos .. of each tile: lane mod kPos looks one up, and the lanes of a
     // line (16 of 16 bytes of bf16, 8 of 16 codes) keep the rows they copy in registers for the tile.
     static constexpr int kPos = F::M / F::load_warps;  // 8, 16 or 32
@@ -453,10 +454,10 @@ struct Loader {
 };
 
 // The queries of a unit by two warps; unused columns and elements past d are zeros.
-template <int C, int N>
+template <int C, int N, bool FP8>
 __device__ __forceinline__ void load_queries(const Kargs &k, const Unit *w, Misc *m, unsigned char *smem, int warp, int lane)
 {
-    using F = Cfg<C, N>;
+    using F = Cfg<C, N, FP8>;
     const int vec = lane & 15, heads = w->heads, cols = w->cols();
     const uint32_t to = smem_addr(smem + F::q_off) + (vec >> 3) * F::q_half;
 #pragma unroll 4
@@ -484,7 +485,7 @@ __device__ __forceinline__ void load_queries(const Kargs &k, const Unit *w, Misc
 // One warp, all lanes in step, one of them issuing.
 template <int C, int N, bool FP8>
 struct Issuer {
-    using F = Cfg<C, N>;
+    using F = Cfg<C, N, FP8>;
     Misc *m;
     const Waiter &wait;
     // descriptors of the ring's first chunk, of the queries and of P; a step adds its offset / 16
@@ -567,9 +568,9 @@ struct Issuer {
 // ------------------------------------------------------------------------------------ softmax
 // Thread t of warp `quad` of a group holds, of a tile's scores, H blocks of 16 positions by the group's
 // columns in the layout of tmem_ld: 2 H positions by 2 G columns.
-template <int C, int N>
+template <int C, int N, bool FP8>
 struct Softmax {
-    using F = Cfg<C, N>;
+    using F = Cfg<C, N, FP8>;
     static constexpr int W = F::cols_per_group, G = W / 8, H = F::M / 64;
     static constexpr int X = 4 * G;  // values of a block of 16 positions
     const Kargs &k;
@@ -606,12 +607,25 @@ struct Softmax {
         return in ? v : -INFINITY;
     }
 
+    __device__ __forceinline__ void mask_all(float x[H][X], const Mask &mask) const
+    {
+#pragma unroll
+        for (int h = 0; h < H; ++h)
+#pragma unroll
+            for (int i = 0; i < X; ++i) x[h][i] = masked(mask, x[h][i], h, i);
+    }
+
     // Scores exceed their columns' references by too much (or a column has none yet): new references, sums
     // and accumulators brought to them, x formed again.
-    __device__ __forceinline__ void move_references(float x[H][X], int buf, bool started, const Mask &mask)
+    __device__ __forceinline__ void move_references(float x[H][X], int buf, bool started, const Mask &mask, bool whole)
     {
         float factor[2 * G];
         load_scores(x, buf);
+#pragma unroll
+        for (int h = 0; h < H; ++h)
+#pragma unroll
+            for (int i = 0; i < X; ++i) x[h][i] *= k.a.scale_log2;
+        if (!whole) mask_all(x, mask);
 #pragma unroll
         for (int c = 0; c < 2 * G; ++c) {
             float top = -INFINITY;
@@ -620,7 +634,7 @@ struct Softmax {
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
                     const int i = (c >> 1) * 4 + r * 2 + (c & 1);
-                    top = fmaxf(top, masked(mask, x[h][i] * k.a.scale_log2, h, i));
+                    top = fmaxf(top, x[h][i]);
                 }
 #pragma unroll
             for (int s = 4; s < 32; s <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
@@ -636,6 +650,13 @@ struct Softmax {
             ref[c] = now;
             sum[c] *= factor[c];
         }
+#pragma unroll
+        for (int h = 0; h < H; ++h)
+#pragma unroll
+            for (int i = 0; i < X; ++i) {
+                const float r = ref[((i >> 2) << 1) | (i & 1)];
+                x[h][i] -= r == -INFINITY ? 0.0f : r;  // (a column without positions: its scores are all -inf)
+            }
         if (started) {
             wait(&m->pv_done[(tile - 1) & 1], ((tile - 1) >> 1) & 1);
             tmem_fence_after();
@@ -651,20 +672,6 @@ struct Softmax {
             }
             tmem_wait_st();
         }
-        subtract(x, mask, true);
-    }
-
-    // x = score * scale - reference: log2 of the weight, -inf where masked.
-    __device__ __forceinline__ void subtract(float x[H][X], const Mask &mask, bool apply) const
-    {
-#pragma unroll
-        for (int h = 0; h < H; ++h)
-#pragma unroll
-            for (int i = 0; i < X; ++i) {
-                const float r = ref[((i >> 2) << 1) | (i & 1)];
-                x[h][i] = fmaf(x[h][i], k.a.scale_log2, -r);
-                if (apply) x[h][i] = masked(mask, x[h][i], h, i);
-            }
     }
 
     // A position that one row attends to and another does not has weight 0 in the other, but 0 * NaN is
@@ -719,20 +726,25 @@ struct Softmax {
             for (int b = 0; b < 2 * H; ++b) mask.valid |= ((word >> (vshift + 8 * b)) & 1u) << b;
             const uint32_t dirty = mask.edges ? take_out(x, mask) : 0u;
             const bool whole = __all_sync(0xffffffffu, mask.valid == (1u << (2 * H)) - 1u) && !mask.edges;
-            subtract(x, mask, false);
-            if (!whole) {
+            // x = score * scale - reference: log2 of the weight, -inf where masked.  The first tile sets the
+            // references, a later one moves them when a score exceeds its own by too much.
+            bool move = it == 0;
+            if (!move) {
+                float top = -INFINITY;
 #pragma unroll
                 for (int h = 0; h < H; ++h)
 #pragma unroll
-                    for (int i = 0; i < X; ++i) x[h][i] = masked(mask, x[h][i], h, i);
+                    for (int i = 0; i < X; ++i)
+                        x[h][i] = fmaf(x[h][i], k.a.scale_log2, -ref[((i >> 2) << 1) | (i & 1)]);
+                if (!whole) mask_all(x, mask);
+#pragma unroll
+                for (int h = 0; h < H; ++h)
+#pragma unroll
+                    for (int i = 0; i < X; ++i) top = fmaxf(top, x[h][i]);
+                // (a column without positions yet has the reference -inf, which any score exceeds)
+                move = bar_any(1 + group, 128, top > kRefSlack);
             }
-            float top = x[0][0];
-#pragma unroll
-            for (int h = 0; h < H; ++h)
-#pragma unroll
-                for (int i = 0; i < X; ++i) top = fmaxf(top, x[h][i]);
-            // (a column without positions yet has the reference -inf, which any score exceeds)
-            if (bar_any(1 + group, 128, top > kRefSlack)) move_references(x, buf, it > 0, mask);
+            if (move) move_references(x, buf, it > 0, mask, whole);
             tmem_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&m->s_empty[buf]);
@@ -749,21 +761,24 @@ struct Softmax {
                 const int before = tile - F::pbufs;
                 wait(&m->pv_done[before & 1], (before >> 1) & 1);
             }
-            unsigned char *p = smem + F::p_off + (tile % F::pbufs) * F::p_bytes + (group * W / 64) * F::p_block +
-                               (lane & 3) * 4;
+            // P^T, four 8 x 8 blocks an instruction: lane i gives the address of line i mod 8 of block i / 8
+            const uint32_t p = smem_addr(smem + F::p_off + (tile % F::pbufs) * F::p_bytes + (group * W / 64) * F::p_block);
+            const int unit0 = (group * W % 64) / 8;
 #pragma unroll
             for (int h = 0; h < H; ++h)
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const int at = line(h, r);
+                for (int g = 0; g < G; g += 2) {
+                    uint32_t out[4];
 #pragma unroll
-                    for (int g = 0; g < G; ++g) {
-                        const float p0 = exp2_approx(x[h][4 * g + 2 * r]), p1 = exp2_approx(x[h][4 * g + 2 * r + 1]);
-                        sum[2 * g] += p0;
-                        sum[2 * g + 1] += p1;
-                        const int unit = (group * W % 64) / 8 + g;
-                        *reinterpret_cast<uint32_t *>(p + at * 128 + ((unit ^ (at & 7)) << 4)) = pack_bf16(p0, p1);
+                    for (int q = 0; q < 4; ++q) {  // block q: columns of g + q / 2, lines 8 (q mod 2) ..
+                        const int gg = g + (q >> 1), i = 4 * gg + 2 * (q & 1);
+                        const float p0 = exp2_approx(x[h][i]), p1 = exp2_approx(x[h][i + 1]);
+                        sum[2 * gg] += p0;
+                        sum[2 * gg + 1] += p1;
+                        out[q] = pack_bf16(p0, p1);
                     }
+                    const int at = quad * (16 * H) + h * 16 + ((lane >> 3) & 1) * 8 + (lane & 7);
+                    stmatrix4(p + at * 128 + (((unit0 + g + (lane >> 4)) ^ (at & 7)) << 4), out);
                 }
             fence_proxy_async_shared();
             tmem_fence_before();
@@ -854,11 +869,15 @@ struct Softmax {
 #pragma unroll
             for (int b = 0; b < 2; ++b)
 #pragma unroll
-                for (int i = 0; i < X; ++i) {
-                    const int c = ((i >> 2) << 1) | (i & 1), j = col(c) - group * W;
-                    const int e = quad * 32 + b * 16 + ((i >> 1) & 1) * 8 + (lane >> 2);
-                    *reinterpret_cast<__nv_bfloat16 *>(stage + j * 256 + (((e >> 3) ^ (j & 15)) << 4) + (e & 7) * 2) =
-                        __float2bfloat16_rn(o[b][i] * inv[c]);
+                for (int g = 0; g < G; g += 2) {
+                    uint32_t out[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {  // as P^T's blocks, stored transposed: 8 elements of a column a line
+                        const int gg = g + (q >> 1), i = 4 * gg + 2 * (q & 1);
+                        out[q] = pack_bf16(o[b][i] * inv[2 * gg], o[b][i + 1] * inv[2 * gg + 1]);
+                    }
+                    const int j = (g + (lane >> 4)) * 8 + (lane & 7), u = quad * 4 + b * 2 + ((lane >> 3) & 1);
+                    stmatrix4_trans(smem_addr(stage) + j * 256 + ((u ^ (j & 15)) << 4), out);
                 }
             bar_sync(bar, 128);
 #pragma unroll
@@ -876,9 +895,9 @@ struct Softmax {
 
 // ------------------------------------------------------------------------------------ the kernel
 template <int C, int N, bool FP8>
-__global__ void __launch_bounds__(Cfg<C, N>::threads, 1) attention_kernel(const __grid_constant__ Kargs k)
+__global__ void __launch_bounds__(Cfg<C, N, FP8>::threads, 1) attention_kernel(const __grid_constant__ Kargs k)
 {
-    using F = Cfg<C, N>;
+    using F = Cfg<C, N, FP8>;
     extern __shared__ __align__(1024) unsigned char smem[];
     Misc *m = reinterpret_cast<Misc *>(smem + F::misc_off);
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
@@ -920,7 +939,7 @@ __global__ void __launch_bounds__(Cfg<C, N>::threads, 1) attention_kernel(const 
         regs_to<F::soft_regs, (F::soft_regs > F::launch_regs)>();
         const int group = warp >> 2, quad = warp & 3;
         const uint32_t at = m->tmem + (static_cast<uint32_t>(quad * 32) << 16) + group * F::cols_per_group;
-        Softmax<C, N> soft{k, m, wait, smem, group, quad, lane, at, at + C * N};
+        Softmax<C, N, FP8> soft{k, m, wait, smem, group, quad, lane, at, at + C * N};
         int i = 0;
         for (int64_t u = blockIdx.x; u < units; u += gridDim.x, ++i) {
             soft.unit(*take(i));
@@ -959,13 +978,13 @@ __global__ void __launch_bounds__(Cfg<C, N>::threads, 1) attention_kernel(const 
                 const Unit *w = take(i);
                 if (w->n > 0) {
                     wait(&m->q_empty, (loaded++ & 1) ^ 1);
-                    load_queries<C, N>(k, w, m, smem, warp - kUnitWarp - 1, lane);
+                    load_queries<C, N, FP8>(k, w, m, smem, warp - kUnitWarp - 1, lane);
                 }
                 give(i);
             }
         }
     } else {
-        regs_to<F::load_regs, true>();
+        regs_to<F::load_regs, (F::load_regs > F::launch_regs)>();
         Loader<C, N, FP8> load{k, m, wait, smem, lane, warp - kLoadWarp0};
         int i = 0;
         for (int64_t u = blockIdx.x; u < units; u += gridDim.x, ++i) {
@@ -1019,7 +1038,7 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Kargs
 template <int C, int N, bool FP8>
 cudaError_t launch(const Kargs &k, cudaStream_t s)
 {
-    using F = Cfg<C, N>;
+    using F = Cfg<C, N, FP8>;
     constexpr size_t smem = F::misc_off + sizeof(Misc);
     static_assert(smem <= 232448, "more than a CTA may use");
     static_assert(smem > 116 * 1024, "one CTA an SM: each takes all of the tensor memory");

@@ -133,6 +133,21 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t *bar)
 }
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
+// Four 8 x 8 blocks of bf16 to shared memory: thread t holds line t / 4, columns 2 (t mod 4) + {0, 1} of
+// block q in v[q]; lane i gives the address of line (transposed: column) i mod 8 of block i / 8.
+__device__ __forceinline__ void stmatrix4(uint32_t addr, const uint32_t v[4])
+{
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]),
+                 "r"(v[2]), "r"(v[3])
+                 : "memory");
+}
+__device__ __forceinline__ void stmatrix4_trans(uint32_t addr, const uint32_t v[4])
+{
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]),
+                 "r"(v[1]), "r"(v[2]), "r"(v[3])
+                 : "memory");
+}
+
 // Barrier `id` over `threads` threads, and over the same threads whether any has `pred`.
 __device__ __forceinline__ void bar_sync(int id, int threads)
 {
