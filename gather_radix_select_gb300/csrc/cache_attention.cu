@@ -9,10 +9,9 @@
 // the value is the key tile itself, read with the other dimension contiguous: each cache row is staged
 // once and used for both products.
 //
-// The sum of exponentials needs no maximum, only a reference that keeps exp2 in range.  `ref` is the
-// column's largest score when it was last set; while no weight exceeds it by more than 2^24 the tile is
-// taken with one vote.  Else the columns' maxima are formed across the positions and the sums and
-// accumulators are rescaled.  Sums are kept per thread (its positions) and joined at the end.
+// The sum of exponentials needs no maximum, only a reference that keeps exp2 in range.  `ref` is set from a
+// column's largest score, with room above; while no weight outgrows it a tile is taken with one vote.  Else
+// the columns' maxima are formed across the positions and the sums and accumulators are rescaled.  Sums are kept per thread (its positions) and joined at the end.
 //
 // A CTA stays on its SM and takes one unit of work (rows x heads x a part of the positions) after the
 // other; its 20 warps are 8 of softmax (two groups of 4: 32 columns each), one that issues the products,
@@ -42,9 +41,10 @@ constexpr int kLoadWarp0 = kSoftWarps + 4;
 constexpr int kMaxRing = 5;
 constexpr int kValidSlots = 16;            // tiles whose validity bits are kept (more than the ring holds)
 constexpr int kMaxSplit = 64;
-// log2 of how far a weight may exceed 1 before its column's reference moves.  bf16 has the range of fp32, so
-// the weights lose nothing by it; products stay finite for values up to 2^100.
-constexpr float kRefSlack = 24.0f;
+// A column's reference is set 2^kHeadroom above its largest weight so far and moves when a weight reaches
+// twice the reference.  bf16 has the range of fp32, so the small weights lose nothing by it, and that
+// a weight is 2 or more is one bit of its bf16 exponent.
+constexpr float kHeadroom = 24.0f;
 constexpr long long kWaitCycles = 4000000000LL;  // about 2 s
 constexpr uint32_t kSuspend = 1000;
 constexpr int32_t kTimeout = 5;            // SEL_ETIMEOUT
@@ -150,6 +150,23 @@ struct Waiter {
     }
 };
 
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    float2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(reinterpret_cast<uint64_t &>(d))
+        : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)), "l"(reinterpret_cast<uint64_t &>(c)));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    float2 d;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<uint64_t &>(d))
+        : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)));
+    return d;
+}
+
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
 {
     const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
@@ -226,41 +243,46 @@ __device__ __forceinline__ void make_unit(const Kargs &k, int64_t u, Unit *w, in
 }
 
 // ------------------------------------------------------------------------------------ staging rows
-// 16 codes times their scale -> 16 bf16 in two 16-byte units.
-__device__ __forceinline__ void decode16(uint4 codes, float scale, uint4 &a, uint4 &b)
+// 8-bit codes to bf16.  With a scale that is a power of two below 2^8 and no NaN among the codes
+// (decodes_fast), a code's exponent and mantissa bits, put where bf16 has them, are its value times 2^-120
+// (subnormal codes give subnormal numbers), and one bf16 product makes that value * scale, rounding only
+// where the result is subnormal.  Else by way of fp32.
+__device__ __forceinline__ bool decodes_fast(uint4 codes, float scale)
 {
-    const uint32_t in[4] = {codes.x, codes.y, codes.z, codes.w};
-    uint32_t out[8];
-    // A power of two below 2^8 and no NaN among the codes: the code's exponent and mantissa bits, put
-    // where bf16 has them, are the value times 2^-120 (subnormal codes give subnormal numbers), and one
-    // bf16 product makes it value * scale, rounding only where the result is subnormal.
     const uint32_t s = __float_as_uint(scale);
-    uint32_t nan = 0;
+    const uint32_t nan = ((codes.x & 0x7f7f7f7fu) + 0x01010101u) | ((codes.y & 0x7f7f7f7fu) + 0x01010101u) |
+                         ((codes.z & 0x7f7f7f7fu) + 0x01010101u) | ((codes.w & 0x7f7f7f7fu) + 0x01010101u);
+    return ((s & 0x007fffffu) | (nan & 0x80808080u)) == 0 && s - 0x00800000u < (134u << 23);
+}
+
+// Codes of a word: two times two bf16.
+__device__ __forceinline__ uint2 decode4_fast(uint32_t codes, uint32_t by2)
+{
+    uint32_t out[2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) nan |= (in[i] & 0x7f7f7f7fu) + 0x01010101u;
-    if ((s & 0x007fffffu) == 0 && s - 0x00800000u < (134u << 23) && (nan & 0x80808080u) == 0) {
-        const uint32_t f = (s >> 16) + (120u << 7), f2 = f | (f << 16);
-        const __nv_bfloat162 by = *reinterpret_cast<const __nv_bfloat162 *>(&f2);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            // bytes to sign-extended halves, shifted to the places of bf16's exponent and mantissa
-            uint32_t y;  // (selector digits from 8 repeat the byte's sign; __byte_perm drops that bit)
-            asm("prmt.b32 %0, %1, 0, %2;" : "=r"(y) : "r"(in[i >> 1]), "r"(i & 1 ? 0xb3a2 : 0x9180));
-            y = (y << 4) & 0x87f087f0u;
-            const __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&y), by);
-            out[i] = *reinterpret_cast<const uint32_t *>(&v);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
-                static_cast<__nv_fp8x2_storage_t>((in[i >> 1] >> (16 * (i & 1))) & 0xffffu), __NV_E4M3);
-            const float2 v = __half22float2(__half2(h));
-            out[i] = pack_bf16(v.x * scale, v.y * scale);
-        }
+    for (int i = 0; i < 2; ++i) {
+        // bytes to sign-extended halves, shifted to the places of bf16's exponent and mantissa
+        uint32_t y;  // (selector digits from 8 repeat the byte's sign; __byte_perm drops that bit)
+        asm("prmt.b32 %0, %1, 0, %2;" : "=r"(y) : "r"(codes), "r"(i ? 0xb3a2 : 0x9180));
+        y = (y << 4) & 0x87f087f0u;
+        const __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&y),
+                                         *reinterpret_cast<const __nv_bfloat162 *>(&by2));
+        out[i] = *reinterpret_cast<const uint32_t *>(&v);
     }
-    a = make_uint4(out[0], out[1], out[2], out[3]);
-    b = make_uint4(out[4], out[5], out[6], out[7]);
+    return make_uint2(out[0], out[1]);
+}
+
+__device__ __forceinline__ uint2 decode4_exact(uint32_t codes, float scale)
+{
+    uint32_t out[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const __half2_raw h =
+            __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>((codes >> (16 * i)) & 0xffffu), __NV_E4M3);
+        const float2 v = __half22float2(__half2(h));
+        out[i] = pack_bf16(v.x * scale, v.y * scale);
+    }
+    return make_uint2(out[0], out[1]);
 }
 
 template <int C, int N, bool FP8>
@@ -418,20 +440,44 @@ struct Loader {
         const int u = (2 * vec) & 7;
         const bool odd = vec >= 4;
         unsigned char *to = smem + (vec >> 2) * F::half_bytes + line0 * 128;
+        // 16 values of a line: units u, u + 1.  Lanes of the second half store their second unit first: the 8
+        // lanes of a line then cover all banks in each of the two stores.
+        auto put = [&](unsigned char *at, int sw, uint4 a, uint4 b) {
+            *reinterpret_cast<uint4 *>(at + (((u + odd) ^ sw) << 4)) = odd ? b : a;
+            *reinterpret_cast<uint4 *>(at + (((u + !odd) ^ sw) << 4)) = odd ? a : b;
+        };
         int sg = 0;  // group of the chunk being stored
         auto store = [&](int g, const Codes &x) {
             if (g >= total) return;
             if (sg == 0) wait(&m->empty[stage], phase);
             unsigned char *base = to + stage * F::chunk_bytes + sg * (kLoads * 4 * 128);
+            bool fast = true;
 #pragma unroll
-            for (int i = 0; i < kLoads; ++i) {
-                uint4 a, b;
-                decode16(x.codes[i], x.scale[i], a, b);
-                const int sw = (line0 + 4 * i) & 7;
-                // lanes of the second half store their second unit first: the 8 lanes of a line then
-                // cover all banks in each of the two stores
-                *reinterpret_cast<uint4 *>(base + i * 512 + (((u + odd) ^ sw) << 4)) = odd ? b : a;
-                *reinterpret_cast<uint4 *>(base + i * 512 + (((u + !odd) ^ sw) << 4)) = odd ? a : b;
+            for (int i = 0; i < kLoads; ++i) fast &= decodes_fast(x.codes[i], x.scale[i]);
+            if (fast) {
+#pragma unroll
+                for (int i = 0; i < kLoads; ++i) {
+                    const uint32_t f = (__float_as_uint(x.scale[i]) >> 16) + (120u << 7), by2 = f | (f << 16);
+                    const uint2 a0 = decode4_fast(x.codes[i].x, by2), a1 = decode4_fast(x.codes[i].y, by2);
+                    const uint2 b0 = decode4_fast(x.codes[i].z, by2), b1 = decode4_fast(x.codes[i].w, by2);
+                    put(base + i * 512, (line0 + 4 * i) & 7, make_uint4(a0.x, a0.y, a1.x, a1.y),
+                        make_uint4(b0.x, b0.y, b1.x, b1.y));
+                }
+            } else {
+#pragma unroll 1
+                for (int i = 0; i < kLoads; ++i) {
+                    uint4 c = x.codes[0];
+                    float f = x.scale[0];
+#pragma unroll
+                    for (int j = 1; j < kLoads; ++j) {
+                        c = i == j ? x.codes[j] : c;
+                        f = i == j ? x.scale[j] : f;
+                    }
+                    const uint2 a0 = decode4_exact(c.x, f), a1 = decode4_exact(c.y, f);
+                    const uint2 b0 = decode4_exact(c.z, f), b1 = decode4_exact(c.w, f);
+                    put(base + i * 512, (line0 + 4 * i) & 7, make_uint4(a0.x, a0.y, a1.x, a1.y),
+                        make_uint4(b0.x, b0.y, b1.x, b1.y));
+                }
             }
             if (++sg < kGroups) return;
             sg = 0;
@@ -495,12 +541,13 @@ struct Issuer {
     int s_stage = 0, s_phase = 0, v_stage = 0;
     int s_tile = 0, v_tile = 0;  // tiles issued so far
 
+    // A tile's scores.
     __device__ __forceinline__ void scores()
     {
         constexpr uint32_t kScores = umma_idesc(F::M, N, false, false);
         const int buf = s_tile & 1;
-        wait(&m->s_empty[buf], ((s_tile >> 1) & 1) ^ 1);
         const uint32_t d = s_col + buf * N;
+        wait(&m->s_empty[buf], ((s_tile >> 1) & 1) ^ 1);
 #pragma unroll 1
         for (int c = 0; c < C; ++c) {
             wait(&m->full[s_stage], s_phase);
@@ -543,11 +590,11 @@ struct Issuer {
                     for (int s = 1; s < F::M / 16; ++s) umma_bf16(d, a + s * 128, b + s * 128, kValues, true);
                 }
                 umma_commit(&m->empty[v_stage]);
+                if (c + 1 == C) umma_commit(&m->pv_done[buf]);
             }
             __syncwarp();
             if (++v_stage == F::ring) v_stage = 0;
         }
-        if (elect_one()) umma_commit(&m->pv_done[buf]);
         ++v_tile;
     }
 
@@ -580,9 +627,8 @@ struct Softmax {
     int group, quad, lane;
     uint32_t o_tm, s_tm;  // the warp's lanes and the group's columns of the accumulators and scores
     int tile = 0;         // tiles done so far
-    float ref[2 * G], sum[2 * G];  // of the thread's columns: reference, sum over its positions
+    float2 neg[G], sum[G];  // of the thread's pairs of columns: minus the reference, sum over its positions
 
-    // (a tile of 64 positions lies in lanes 0 .. 15 of each warp's 32)
     __device__ __forceinline__ int line(int h, int r) const { return quad * (16 * H) + h * 16 + r * 8 + (lane >> 2); }
     __device__ __forceinline__ int col(int i) const { return group * W + (i >> 1) * 8 + (lane & 3) * 2 + (i & 1); }
 
@@ -615,11 +661,11 @@ struct Softmax {
             for (int i = 0; i < X; ++i) x[h][i] = masked(mask, x[h][i], h, i);
     }
 
-    // Scores exceed their columns' references by too much (or a column has none yet): new references, sums
-    // and accumulators brought to them, x formed again.
+    // Weights outgrow their columns' references (or a column has none yet): new references, sums and
+    // accumulators brought to them, the scores loaded again.
     __device__ __forceinline__ void move_references(float x[H][X], int buf, bool started, const Mask &mask, bool whole)
     {
-        float factor[2 * G];
+        float2 factor[G];
         load_scores(x, buf);
 #pragma unroll
         for (int h = 0; h < H; ++h)
@@ -632,31 +678,26 @@ struct Softmax {
 #pragma unroll
             for (int h = 0; h < H; ++h)
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const int i = (c >> 1) * 4 + r * 2 + (c & 1);
-                    top = fmaxf(top, x[h][i]);
-                }
+                for (int r = 0; r < 2; ++r) top = fmaxf(top, x[h][(c >> 1) * 4 + r * 2 + (c & 1)]);
 #pragma unroll
             for (int s = 4; s < 32; s <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
             if (lane < 4) m->part[quad][col(c)] = top;
         }
         bar_sync(1 + group, 128);
-#pragma unroll
-        for (int c = 0; c < 2 * G; ++c) {
+        auto moved = [&](int c, float &n, float &sum_of) {
             const int at = col(c);
-            const float now = fmaxf(fmaxf(ref[c], fmaxf(m->part[0][at], m->part[1][at])),
-                                    fmaxf(m->part[2][at], m->part[3][at]));
-            factor[c] = ref[c] == now ? 1.0f : exp2_approx(ref[c] - now);
-            ref[c] = now;
-            sum[c] *= factor[c];
+            const float top = fmaxf(fmaxf(m->part[0][at], m->part[1][at]), fmaxf(m->part[2][at], m->part[3][at]));
+            const float now = fmaxf(-n, top + kHeadroom);
+            const float f = -n == now ? 1.0f : exp2_approx(-n - now);
+            n = -now;
+            sum_of *= f;
+            return f;
+        };
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            factor[g].x = moved(2 * g, neg[g].x, sum[g].x);
+            factor[g].y = moved(2 * g + 1, neg[g].y, sum[g].y);
         }
-#pragma unroll
-        for (int h = 0; h < H; ++h)
-#pragma unroll
-            for (int i = 0; i < X; ++i) {
-                const float r = ref[((i >> 2) << 1) | (i & 1)];
-                x[h][i] -= r == -INFINITY ? 0.0f : r;  // (a column without positions: its scores are all -inf)
-            }
         if (started) {
             wait(&m->pv_done[(tile - 1) & 1], ((tile - 1) >> 1) & 1);
             tmem_fence_after();
@@ -667,11 +708,44 @@ struct Softmax {
                 tmem_ld<G>(at, o);
                 tmem_wait_ld();
 #pragma unroll
-                for (int i = 0; i < X; ++i) o[i] *= factor[((i >> 2) << 1) | (i & 1)];
+                for (int i = 0; i < X; ++i) o[i] *= (i & 1) ? factor[i >> 2].y : factor[i >> 2].x;
                 tmem_st<G>(at, o);
             }
             tmem_wait_st();
         }
+        load_scores(x, buf);
+    }
+
+    // A tile's weights 2^(score * scale - reference), two positions by G pairs of columns a block, as bf16
+    // pairs; added to `to`.  Returns whether one is 2 or more (or NaN).
+    __device__ __forceinline__ bool weights(const float x[H][X], const Mask &mask, bool whole, uint32_t dirty,
+                                            uint32_t out[H][2 * G], float2 to[G]) const
+    {
+        const float2 scale = make_float2(k.a.scale_log2, k.a.scale_log2);
+        uint32_t any = 0;
+#pragma unroll
+        for (int h = 0; h < H; ++h)
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const int i = 4 * g + 2 * r;
+                    float2 y = fma2(make_float2(x[h][i], x[h][i + 1]), scale, neg[g]);
+                    if (!whole) {
+                        // (a column without positions has no finite reference: its scores are all masked)
+                        y.x = masked(mask, y.x, h, i);
+                        y.y = masked(mask, y.y, h, i + 1);
+                        if ((dirty >> (2 * h + r)) & 1u) {
+                            y.x = y.x != -INFINITY ? __int_as_float(0x7fffffff) : y.x;
+                            y.y = y.y != -INFINITY ? __int_as_float(0x7fffffff) : y.y;
+                        }
+                    }
+                    const float2 p = make_float2(exp2_approx(y.x), exp2_approx(y.y));
+                    to[g] = add2(to[g], p);
+                    out[h][2 * g + r] = pack_bf16(p.x, p.y);
+                    any |= out[h][2 * g + r];
+                }
+        return (any & 0x40004000u) != 0;
     }
 
     // A position that one row attends to and another does not has weight 0 in the other, but 0 * NaN is
@@ -726,36 +800,24 @@ struct Softmax {
             for (int b = 0; b < 2 * H; ++b) mask.valid |= ((word >> (vshift + 8 * b)) & 1u) << b;
             const uint32_t dirty = mask.edges ? take_out(x, mask) : 0u;
             const bool whole = __all_sync(0xffffffffu, mask.valid == (1u << (2 * H)) - 1u) && !mask.edges;
-            // x = score * scale - reference: log2 of the weight, -inf where masked.  The first tile sets the
-            // references, a later one moves them when a score exceeds its own by too much.
-            bool move = it == 0;
-            if (!move) {
-                float top = -INFINITY;
+            // the first tile sets the references, a later one moves them when a weight outgrows its own
+            if (it == 0) move_references(x, buf, false, mask, whole);
+            uint32_t out[H][2 * G];
+            float2 to[G];
 #pragma unroll
-                for (int h = 0; h < H; ++h)
+            for (int g = 0; g < G; ++g) to[g] = sum[g];
+            const bool over = weights(x, mask, whole, dirty, out, to);
+            if (it > 0 && bar_any(1 + group, 128, over)) {
+                move_references(x, buf, true, mask, whole);
 #pragma unroll
-                    for (int i = 0; i < X; ++i)
-                        x[h][i] = fmaf(x[h][i], k.a.scale_log2, -ref[((i >> 2) << 1) | (i & 1)]);
-                if (!whole) mask_all(x, mask);
-#pragma unroll
-                for (int h = 0; h < H; ++h)
-#pragma unroll
-                    for (int i = 0; i < X; ++i) top = fmaxf(top, x[h][i]);
-                // (a column without positions yet has the reference -inf, which any score exceeds)
-                move = bar_any(1 + group, 128, top > kRefSlack);
+                for (int g = 0; g < G; ++g) to[g] = sum[g];
+                weights(x, mask, whole, dirty, out, to);
             }
-            if (move) move_references(x, buf, it > 0, mask, whole);
+#pragma unroll
+            for (int g = 0; g < G; ++g) sum[g] = to[g];
             tmem_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&m->s_empty[buf]);
-            if (dirty) {
-#pragma unroll
-                for (int h = 0; h < H; ++h)
-#pragma unroll
-                    for (int i = 0; i < X; ++i)
-                        if (((dirty >> (2 * h + ((i >> 1) & 1))) & 1u) && x[h][i] != -INFINITY)
-                            x[h][i] = __int_as_float(0x7fffffff);
-            }
             // the buffer of P is free once the product that read it is done
             if (tile >= F::pbufs) {
                 const int before = tile - F::pbufs;
@@ -768,17 +830,8 @@ struct Softmax {
             for (int h = 0; h < H; ++h)
 #pragma unroll
                 for (int g = 0; g < G; g += 2) {
-                    uint32_t out[4];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {  // block q: columns of g + q / 2, lines 8 (q mod 2) ..
-                        const int gg = g + (q >> 1), i = 4 * gg + 2 * (q & 1);
-                        const float p0 = exp2_approx(x[h][i]), p1 = exp2_approx(x[h][i + 1]);
-                        sum[2 * gg] += p0;
-                        sum[2 * gg + 1] += p1;
-                        out[q] = pack_bf16(p0, p1);
-                    }
                     const int at = quad * (16 * H) + h * 16 + ((lane >> 3) & 1) * 8 + (lane & 7);
-                    stmatrix4(p + at * 128 + (((unit0 + g + (lane >> 4)) ^ (at & 7)) << 4), out);
+                    stmatrix4(p + at * 128 + (((unit0 + g + (lane >> 4)) ^ (at & 7)) << 4), out[h] + 2 * g);
                 }
             fence_proxy_async_shared();
             tmem_fence_before();
@@ -792,18 +845,19 @@ struct Softmax {
         const int bar = 1 + group, cols = w.cols(), n = w.n;
         auto out_row = [&](int c) { return static_cast<int64_t>(w.out[c]); };
 #pragma unroll
-        for (int c = 0; c < 2 * G; ++c) {
-            ref[c] = -INFINITY;
-            sum[c] = 0.0f;
+        for (int g = 0; g < G; ++g) {
+            neg[g] = make_float2(INFINITY, INFINITY);
+            sum[g] = make_float2(0.0f, 0.0f);
         }
         tiles(w);
         // column sums, in a fixed order
         bar_sync(bar, 128);
 #pragma unroll
         for (int c = 0; c < 2 * G; ++c) {
+            float l = (c & 1) ? sum[c >> 1].y : sum[c >> 1].x;
 #pragma unroll
-            for (int s = 4; s < 32; s <<= 1) sum[c] += __shfl_xor_sync(0xffffffffu, sum[c], s);
-            if (lane < 4) m->part[quad][col(c)] = sum[c];
+            for (int s = 4; s < 32; s <<= 1) l += __shfl_xor_sync(0xffffffffu, l, s);
+            if (lane < 4) m->part[quad][col(c)] = l;
         }
         bar_sync(bar, 128);
         if (quad == 0 && lane < 4) {
@@ -811,12 +865,13 @@ struct Softmax {
             for (int c = 0; c < 2 * G; ++c) {
                 const int at = col(c);
                 const float l = (m->part[0][at] + m->part[1][at]) + (m->part[2][at] + m->part[3][at]);
+                const float ref = (c & 1) ? -neg[c >> 1].y : -neg[c >> 1].x;
                 m->inv[at] = l == 0.0f ? 0.0f : 1.0f / l;
                 if (at < cols) {
                     if (k.p.parts > 1)
-                        k.part_ml[out_row(at) * k.p.parts + w.part] = make_float2(ref[c], l);
+                        k.part_ml[out_row(at) * k.p.parts + w.part] = make_float2(ref, l);
                     else if (k.a.lse)
-                        k.a.lse[out_row(at)] = l == 0.0f ? -INFINITY : (ref[c] + log2f(l)) * 0.69314718055994531f;
+                        k.a.lse[out_row(at)] = l == 0.0f ? -INFINITY : (ref + log2f(l)) * 0.69314718055994531f;
                 }
             }
         }
