@@ -80,6 +80,8 @@ def library_path() -> str:
 def load(build_if_missing: bool = False):
     """Load libsel.so once.  Raises RuntimeError when it is not built."""
     global _lib
+    if _lib is not None:  # (without the lock: set once, when the library is complete)
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib

@@ -11,7 +11,6 @@ call belongs to sequence ``r // (rows // b)``.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 
@@ -24,77 +23,85 @@ _IDX = {torch.int32: _native.SEL_I32, torch.int64: _native.SEL_I64}
 _ROWS = {torch.float32: _native.SEL_F32, torch.bfloat16: _native.SEL_BF16}
 
 
-def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+_CACHES = {torch.bfloat16: _native.SEL_BF16, torch.float8_e4m3fn: _native.SEL_E4M3}
 
 
 def _flag(err_flag, dev):
-    if err_flag is not None and (err_flag.dtype != torch.int32 or err_flag.numel() < 1 or err_flag.device != dev):
+    if err_flag is None:
+        return None
+    if err_flag.dtype != torch.int32 or err_flag.numel() < 1 or err_flag.device != dev:
         raise ValueError("err_flag must be an int32 tensor on the cache's device")
-    return _ptr(err_flag)
+    return err_flag.data_ptr()
 
 
 def _cache_struct(cache, scales):
     """The C struct of a cache, and the tensors' checks."""
-    if cache.dim() != 3 or cache.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+    kind = _CACHES.get(cache.dtype)
+    if kind is None or cache.dim() != 3:
         raise ValueError("cache must be a 3-D bfloat16 or float8_e4m3fn tensor [pages, page_size, d]")
     if not cache.is_cuda:
         raise ValueError("cache must be a CUDA tensor")
     pages, page_size, d = cache.shape
-    if d > 1 and cache.stride(2) != 1:
+    page_stride, row_stride, one = cache.stride()
+    if one != 1 and d > 1:
         raise ValueError("cache rows must be contiguous in their last dimension")
-    c = _native.SelCache()
-    c.data = cache.data_ptr()
-    c.pages, c.page_size, c.d = pages, page_size, d
-    c.row_stride = cache.stride(1) if page_size > 1 else d
-    c.page_stride = cache.stride(0) if pages > 1 else page_size * c.row_stride
-    if cache.dtype == torch.bfloat16:
+    if page_size == 1:
+        row_stride = d
+    if pages == 1:
+        page_stride = page_size * row_stride
+    if kind == _native.SEL_BF16:
         if scales is not None:
             raise ValueError("a bfloat16 cache has no scales")
-        c.dtype = _native.SEL_BF16
-        return c
-    c.dtype = _native.SEL_E4M3
+        return _native.SelCache(cache.data_ptr(), None, kind, pages, page_size, d, page_stride, row_stride, 0, 0)
     runs = -(-d // GROUP)
-    if scales is None or scales.dtype != torch.float32 or tuple(scales.shape) != (pages, page_size, runs) \
+    if scales is None or scales.dtype != torch.float32 or scales.shape != (pages, page_size, runs) \
             or scales.device != cache.device:
         raise ValueError("a float8_e4m3fn cache needs float32 scales [pages, page_size, ceil(d / %d)] on its device"
                          % GROUP)
-    if runs > 1 and scales.stride(2) != 1:
+    s_page, s_row, one = scales.stride()
+    if one != 1 and runs > 1:
         raise ValueError("scales must be contiguous in their last dimension")
-    c.scales = scales.data_ptr()
-    c.scale_row_stride = scales.stride(1) if page_size > 1 else runs
-    c.scale_page_stride = scales.stride(0) if pages > 1 else page_size * c.scale_row_stride
-    return c
+    if page_size == 1:
+        s_row = runs
+    if pages == 1:
+        s_page = page_size * s_row
+    return _native.SelCache(cache.data_ptr(), scales.data_ptr(), kind, pages, page_size, d, page_stride, row_stride,
+                            s_page, s_row)
 
 
 def _table(page_table, dev):
-    if page_table.dim() != 2 or page_table.dtype != torch.int32 or page_table.device != dev:
+    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.device != dev:
         raise ValueError("page_table must be an int32 tensor [b, max_pages] on the cache's device")
-    if page_table.shape[0] < 1:
-        raise ValueError("page_table needs a row for each sequence")
-    if page_table.shape[1] > 1 and page_table.stride(1) != 1:
-        raise ValueError("page_table rows must be contiguous")
     b, m = page_table.shape
-    return b, m, page_table.stride(0) if b > 1 else m
+    if b < 1:
+        raise ValueError("page_table needs a row for each sequence")
+    stride, one = page_table.stride()
+    if one != 1 and m > 1:
+        raise ValueError("page_table rows must be contiguous")
+    return b, m, stride if b > 1 else m
 
 
 def _index(idx, dev):
-    if idx.dim() != 2 or idx.dtype not in _IDX or idx.device != dev:
+    if idx.dtype not in _IDX or idx.dim() != 2 or idx.device != dev:
         raise ValueError("idx must be a 2-D int32/int64 tensor on the cache's device")
-    if idx.size(1) > 1 and idx.stride(1) != 1:
+    rows, n = idx.shape
+    stride, one = idx.stride()
+    if one != 1 and n > 1:
         raise ValueError("idx rows must be contiguous")
-    return idx.stride(0) if idx.size(0) > 1 else idx.size(1)
+    return rows, n, stride if rows > 1 else n
 
 
-@contextlib.contextmanager
-def _on(dev, stream):
-    """The device, and the stream to launch and allocate on (so that outputs and scratch belong to it)."""
+def _launch(dev, stream, call):
+    """``call(raw stream)`` with ``dev`` current and, where a stream is given, that stream current too (so that
+    what the call allocates belongs to it)."""
+    if stream is not None:
+        with torch.cuda.device(dev), torch.cuda.stream(stream):
+            return call(stream.cuda_stream)
+    index = dev.index
+    if index == torch.cuda.current_device():  # (the two context managers cost several microseconds)
+        return call(torch._C._cuda_getCurrentRawStream(index))
     with torch.cuda.device(dev):
-        if stream is None:
-            yield ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
-        else:
-            with torch.cuda.stream(stream):
-                yield ctypes.c_void_p(stream.cuda_stream)
+        return call(torch._C._cuda_getCurrentRawStream(index))
 
 
 def cache_write(x: torch.Tensor, cache: torch.Tensor, slots: torch.Tensor, *, scales: torch.Tensor | None = None,
@@ -109,20 +116,21 @@ def cache_write(x: torch.Tensor, cache: torch.Tensor, slots: torch.Tensor, *, sc
     """
     c = _cache_struct(cache, scales)
     dev = cache.device
-    if x.dim() != 2 or x.dtype not in _ROWS or x.device != dev or x.shape[1] != cache.shape[2]:
+    x_type = _ROWS.get(x.dtype)
+    if x_type is None or x.dim() != 2 or x.device != dev or x.shape[1] != c.d:
         raise ValueError("x must be a bfloat16 or float32 tensor [tokens, d] on the cache's device")
-    if x.size(1) > 1 and x.stride(1) != 1:
+    tokens, d = x.shape
+    x_stride, one = x.stride()
+    if one != 1 and d > 1:
         raise ValueError("rows of x must be contiguous")
-    tokens = x.shape[0]
-    if slots.dim() != 1 or slots.dtype not in _IDX or slots.numel() != tokens or slots.device != dev \
+    slot_type = _IDX.get(slots.dtype)
+    if slot_type is None or slots.dim() != 1 or slots.shape[0] != tokens or slots.device != dev \
             or not slots.is_contiguous():
         raise ValueError("slots must be a contiguous int32/int64 tensor with one entry per token")
     err = _flag(err_flag, dev)
-    with _on(dev, stream) as s:
-        st = _native.load().sel_cache_write(
-            _ptr(x), _ROWS[x.dtype], tokens, x.stride(0) if tokens > 1 else x.shape[1], _ptr(slots),
-            _IDX[slots.dtype], ctypes.byref(c), err, s)
-    _native.check(st, "sel_cache_write")
+    _native.check(_launch(dev, stream, lambda s: _native.load().sel_cache_write(
+        x.data_ptr(), x_type, tokens, x_stride if tokens > 1 else d, slots.data_ptr(), slot_type, c, err, s)),
+        "sel_cache_write")
 
 
 def cache_gather(cache: torch.Tensor, page_table: torch.Tensor, idx: torch.Tensor, *,
@@ -135,22 +143,23 @@ def cache_gather(cache: torch.Tensor, page_table: torch.Tensor, idx: torch.Tenso
     """
     c = _cache_struct(cache, scales)
     dev = cache.device
-    b, m, ts = _table(page_table, dev)
-    irs = _index(idx, dev)
-    rows, n = idx.shape
-    d = cache.shape[2]
+    b, m, table_stride = _table(page_table, dev)
+    rows, n, idx_stride = _index(idx, dev)
+    d = c.d
     if out is not None and (out.shape != (rows, n, d) or not out.is_contiguous() or out.dtype != torch.bfloat16
                             or out.device != dev):
         raise ValueError("out must be a contiguous bf16 [rows, n, d] tensor")
     err = _flag(err_flag, dev)
-    with _on(dev, stream) as s:
-        if out is None:
-            out = torch.empty((rows, n, d), dtype=torch.bfloat16, device=dev)
-        st = _native.load().sel_cache_gather(
-            ctypes.byref(c), _ptr(page_table), b, m, ts, _ptr(idx), _IDX[idx.dtype], rows, n, irs, _ptr(out),
-            err, s)
+
+    def call(s):
+        to = cache.new_empty((rows, n, d), dtype=torch.bfloat16) if out is None else out
+        return _native.load().sel_cache_gather(
+            c, page_table.data_ptr(), b, m, table_stride, idx.data_ptr(), _IDX[idx.dtype], rows, n, idx_stride,
+            to.data_ptr(), err, s), to
+
+    st, to = _launch(dev, stream, call)
     _native.check(st, "sel_cache_gather")
-    return out
+    return to
 
 
 def cache_attention(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tensor, *,
@@ -171,41 +180,45 @@ def cache_attention(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tens
     """
     c = _cache_struct(cache, scales)
     dev = cache.device
-    b, m, ts = _table(page_table, dev)
-    d = cache.shape[2]
-    if q.dim() != 3 or q.dtype != torch.bfloat16 or q.device != dev or q.shape[2] != d:
+    b, m, table_stride = _table(page_table, dev)
+    d = c.d
+    if q.dtype != torch.bfloat16 or q.dim() != 3 or q.device != dev or q.shape[2] != d:
         raise ValueError("q must be a bfloat16 tensor [rows, h, d] on the cache's device")
-    if d > 1 and q.stride(2) != 1:
-        raise ValueError("q must be contiguous in its last dimension")
     rows, h, _ = q.shape
-    if end is not None and (end.dtype != torch.int32 or end.dim() != 1 or end.numel() != rows or end.device != dev
+    q_row, q_head, one = q.stride()
+    if one != 1 and d > 1:
+        raise ValueError("q must be contiguous in its last dimension")
+    if end is not None and (end.dtype != torch.int32 or end.dim() != 1 or end.shape[0] != rows or end.device != dev
                             or not end.is_contiguous()):
         raise ValueError("end must be a contiguous int32 tensor with one entry per row")
     dv = d if dv is None else int(dv)
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
-    irs = n = itype = 0
+    n = idx_stride = idx_type = 0
+    idx_ptr = None
     if idx is not None:
-        irs = _index(idx, dev)
-        if idx.shape[0] != rows:
+        listed, n, idx_stride = _index(idx, dev)
+        if listed != rows:
             raise ValueError("idx must have one row per row of q")
-        n, itype = idx.shape[1], _IDX[idx.dtype]
+        idx_type = _IDX[idx.dtype]
+        # an empty list has no address of its own: any address says that idx was given
+        idx_ptr = idx.data_ptr() if n > 0 else page_table.data_ptr() or q.data_ptr()
     if out is not None and (out.shape != (rows, h, dv) or not out.is_contiguous() or out.dtype != torch.bfloat16
                             or out.device != dev):
         raise ValueError("out must be a contiguous bf16 [rows, h, dv] tensor")
     err = _flag(err_flag, dev)
-    lib = _native.load()
-    # an empty index list has no address of its own: any address says that idx was given
-    ip = None if idx is None else (_ptr(idx) if n > 0 else _ptr(page_table) or _ptr(q))
-    with _on(dev, stream) as s:
-        if out is None:
-            out = torch.empty((rows, h, max(dv, 0)), dtype=torch.bfloat16, device=dev)
-        lse = torch.empty((rows, h), dtype=torch.float32, device=dev) if return_lse else None
-        need = int(lib.sel_cache_attention_workspace_size(rows, h, d, dv, b, m, cache.shape[1], int(idx is not None),
-                                                          n))
-        ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-        st = lib.sel_cache_attention(
-            _ptr(q), rows, h, q.stride(0) if rows > 1 else h * d, q.stride(1) if h > 1 else d, ctypes.byref(c),
-            _ptr(page_table), b, m, ts, _ptr(end), ip, itype, n, irs, dv, scale, _ptr(out), _ptr(lse), _ptr(ws),
-            need, err, s)
+
+    def call(s):
+        lib = _native.load()
+        to = q.new_empty((rows, h, max(dv, 0))) if out is None else out
+        lse = q.new_empty((rows, h), dtype=torch.float32) if return_lse else None
+        need = lib.sel_cache_attention_workspace_size(rows, h, d, dv, b, m, c.page_size, idx_ptr is not None, n)
+        ws = q.new_empty(need, dtype=torch.uint8) if need else None
+        return lib.sel_cache_attention(
+            q.data_ptr(), rows, h, q_row if rows > 1 else h * d, q_head if h > 1 else d, c, page_table.data_ptr(),
+            b, m, table_stride, None if end is None else end.data_ptr(), idx_ptr, idx_type, n, idx_stride, dv,
+            scale, to.data_ptr(), None if lse is None else lse.data_ptr(), None if ws is None else ws.data_ptr(),
+            need, err, s), to, lse
+
+    st, to, lse = _launch(dev, stream, call)
     _native.check(st, "sel_cache_attention")
-    return out, lse
+    return to, lse

@@ -15,9 +15,9 @@
 namespace sel {
 namespace {
 
-constexpr int kWriteThreads = 256;
+constexpr int kWriteThreads = 128;
 constexpr int kWriteLanes = 16;   // lanes of one run of 128 elements, 8 elements each
-constexpr int kGatherPairs = 128; // positions of one row handled by one CTA
+constexpr int kGatherPairs = 128; // positions of one row handled by one CTA at most
 
 __device__ __forceinline__ void load8(const void *x, bool bf16, int64_t at, float v[8])
 {
@@ -37,48 +37,68 @@ __device__ __forceinline__ void load8(const void *x, bool bf16, int64_t at, floa
     }
 }
 
-// One run of 128 elements of one token by 16 lanes.
-__global__ void __launch_bounds__(kWriteThreads) cache_write_kernel(const CacheWriteArgs a, uint32_t runs)
+// a / b for 32-bit a; shift: log2(b), or -1 when b is no power of two.
+__device__ __forceinline__ uint32_t quotient(uint32_t a, uint32_t b, int shift) { return shift >= 0 ? a >> shift : a / b; }
+
+// One run of 128 elements of one token by 16 lanes.  The elements are on their way while the slot is read.
+// Instructions bound this kernel (ncu: 59% of the issue slots at 17% of the DRAM bandwidth before the
+// divisions by powers of two became shifts and the magnitudes a floating-point maximum).
+__global__ void __launch_bounds__(kWriteThreads) cache_write_kernel(const CacheWriteArgs a, uint32_t runs, int runs_shift,
+                                                                    int page_shift, uint32_t items)
 {
     const uint32_t lane = threadIdx.x & (kWriteLanes - 1);
-    const int64_t item = (static_cast<int64_t>(blockIdx.x) * kWriteThreads + threadIdx.x) / kWriteLanes;
-    const int64_t token = item / runs;
-    const uint32_t run = static_cast<uint32_t>(item - token * runs);
     const unsigned half = 0xffffu << (threadIdx.x & 16);  // this run's lanes of the warp
-    if (token >= a.tokens) return;
-    const int64_t slot = a.slots_i64 ? static_cast<const int64_t *>(a.slots)[token]
-                                     : static_cast<int64_t>(static_cast<const int32_t *>(a.slots)[token]);
-    if (slot < 0) return;
-    const int64_t page = slot / a.c.page_size, place = slot - page * a.c.page_size;
-    if (page >= a.c.pages) {
-        if (lane == 0 && run == 0 && a.err_flag) atomicCAS(a.err_flag, 0, kCacheInval);
-        return;
-    }
-    const int64_t e = static_cast<int64_t>(run) * kCacheGroup + lane * 8;
+    const uint32_t item = (blockIdx.x * kWriteThreads + threadIdx.x) / kWriteLanes;
+    if (item >= items) return;
+    const uint32_t token = quotient(item, runs, runs_shift), run = item - token * runs;
+    const uint32_t e = run * kCacheGroup + lane * 8;
     const bool in = e < a.c.d;
     float v[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = 0.0f;
     if (in) load8(a.x, a.x_bf16 != 0, token * a.x_stride + e, v);
-    const int64_t row = page * a.c.page_stride + place * a.c.row_stride;
+    const int64_t slot = a.slots_i64 ? __ldg(static_cast<const int64_t *>(a.slots) + token)
+                                     : static_cast<int64_t>(__ldg(static_cast<const int32_t *>(a.slots) + token));
+    if (slot < 0) return;
+    int64_t page, place;
+    if (((slot | a.c.page_size) >> 32) == 0) {  // the common case, without the 64-bit division
+        const uint32_t s = static_cast<uint32_t>(slot), ps = static_cast<uint32_t>(a.c.page_size);
+        const uint32_t q = quotient(s, ps, page_shift);
+        page = q;
+        place = s - q * ps;
+    } else {
+        page = slot / a.c.page_size;
+        place = slot - page * a.c.page_size;
+    }
+    if (page >= a.c.pages) {
+        if (lane == 0 && run == 0 && a.err_flag) atomicCAS(a.err_flag, 0, kCacheInval);
+        return;
+    }
+    const int64_t at = page * a.c.page_stride + place * a.c.row_stride + e;
     if (!a.c.scales) {
         if (in) {
             __nv_bfloat162 o[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) o[i] = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.c.data) + row + e) = *reinterpret_cast<uint4 *>(o);
+            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.c.data) + at) = *reinterpret_cast<uint4 *>(o);
         }
         return;
     }
-    uint32_t top = 0;  // bits of the largest finite magnitude
+    // the largest finite magnitude (a maximum passes over NaN; with an infinity it is formed again without)
+    float top = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const uint32_t m = __float_as_uint(v[i]) & 0x7fffffffu;
-        top = max(top, m < 0x7f800000u ? m : 0u);
+    for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(v[i]));
+#pragma unroll
+    for (int s = kWriteLanes / 2; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(half, top, s));
+    if (isinf(top)) {
+        top = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top = fmaxf(top, isinf(v[i]) ? 0.0f : fabsf(v[i]));
+#pragma unroll
+        for (int s = kWriteLanes / 2; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(half, top, s));
     }
-#pragma unroll
-    for (int s = kWriteLanes / 2; s > 0; s >>= 1) top = max(top, __shfl_xor_sync(half, top, s));
-    int power = static_cast<int>(top >> 23) - 127 - 8 + ((top & 0x7fffffu) > 0x600000u ? 1 : 0);
+    const uint32_t bits = __float_as_uint(top);
+    int power = static_cast<int>(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);
     power = max(power, -126);
     const float inv = __uint_as_float(static_cast<uint32_t>(127 - power) << 23);
     if (in) {
@@ -91,7 +111,7 @@ __global__ void __launch_bounds__(kWriteThreads) cache_write_kernel(const CacheW
                                                          __NV_SATFINITE, __NV_E4M3);
             o[i] = lo | (hi << 16);
         }
-        *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(a.c.data) + row + e) = make_uint2(o[0], o[1]);
+        *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(a.c.data) + at) = make_uint2(o[0], o[1]);
     }
     if (lane == 0)
         a.c.scales[page * a.c.scale_page_stride + place * a.c.scale_row_stride + run] =
@@ -121,8 +141,8 @@ __global__ void __launch_bounds__(kGatherThreads) cache_gather_kernel(const Cach
     __shared__ int64_t s_row[kGatherPairs];    // element offset of the cache row, -1: none
     __shared__ int64_t s_scale[kGatherPairs];
     const int64_t row = blockIdx.x / a.ctas_per_row;
-    const int64_t j0 = (blockIdx.x - row * a.ctas_per_row) * kGatherPairs;
-    const int np = static_cast<int>(a.n - j0 < kGatherPairs ? a.n - j0 : kGatherPairs);
+    const int64_t j0 = (blockIdx.x - row * a.ctas_per_row) * a.pairs;
+    const int np = static_cast<int>(a.n - j0 < a.pairs ? a.n - j0 : a.pairs);
     const int64_t seq = row / a.t.rows_per_seq;
     for (int i = threadIdx.x; i < np; i += kGatherThreads) {
         const int64_t off = row * a.idx_row_stride + j0 + i;
@@ -182,17 +202,29 @@ __global__ void __launch_bounds__(kGatherThreads) cache_gather_kernel(const Cach
 cudaError_t launch_cache_write(const CacheWriteArgs &a, cudaStream_t s)
 {
     const int64_t runs = (a.c.d + kCacheGroup - 1) / kCacheGroup;
-    const int64_t grid = (a.tokens * runs * kWriteLanes + kWriteThreads - 1) / kWriteThreads;
+    const int64_t items = a.tokens * runs, grid = (items * kWriteLanes + kWriteThreads - 1) / kWriteThreads;
     if (grid <= 0) return cudaSuccess;
-    if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
-    cache_write_kernel<<<static_cast<unsigned>(grid), kWriteThreads, 0, s>>>(a, static_cast<uint32_t>(runs));
+    if (items > 0x7fffffffLL / kWriteLanes) return cudaErrorInvalidValue;
+    auto shift_of = [](int64_t n) {
+        int s = 0;
+        while (s < 31 && (int64_t{1} << s) < n) ++s;
+        return (int64_t{1} << s) == n ? s : -1;
+    };
+    cache_write_kernel<<<static_cast<unsigned>(grid), kWriteThreads, 0, s>>>(
+        a, static_cast<uint32_t>(runs), shift_of(runs), shift_of(a.c.page_size), static_cast<uint32_t>(items));
     return cudaGetLastError();
 }
 
 cudaError_t launch_cache_gather(const CacheGatherArgs &a_in, cudaStream_t s)
 {
     CacheGatherArgs a = a_in;
-    a.ctas_per_row = static_cast<int32_t>((a.n + kGatherPairs - 1) / kGatherPairs);
+    // few positions: fewer a CTA, down to 8, so that there are some CTAs for every SM (16 rows x 512 positions
+    // of 512 elements: see DESIGN)
+    const int64_t sms = device_sm_count() > 0 ? device_sm_count() : 1;
+    int64_t pairs = kGatherPairs;
+    while (pairs > 8 && a.rows * ((a.n + pairs - 1) / pairs) < 4 * sms) pairs /= 2;
+    a.pairs = static_cast<int32_t>(pairs);
+    a.ctas_per_row = static_cast<int32_t>((a.n + pairs - 1) / pairs);
     const int64_t grid = a.rows * a.ctas_per_row;
     if (grid <= 0) return cudaSuccess;
     if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;

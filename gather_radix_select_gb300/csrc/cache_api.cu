@@ -100,7 +100,7 @@ int sel_cache_write(const void *x, int x_dtype, int64_t tokens, int64_t x_stride
     if (!aligned(x, 16) || (tokens > 1 && (x_stride * e) % 16 != 0)) return SEL_EALIGN;
     if (!aligned(slots, slot_dtype == SEL_I64 ? 8 : 4)) return SEL_EALIGN;
     const int64_t runs = (cache->d + SEL_CACHE_GROUP - 1) / SEL_CACHE_GROUP;
-    if (tokens > kIntMax / runs) return SEL_EUNSUPPORTED;
+    if (tokens > kIntMax / (16 * runs)) return SEL_EUNSUPPORTED;  // (16 lanes a run, 32-bit counts)
     sel::CacheWriteArgs a{};
     a.c = ref_of(cache);
     a.x = x;

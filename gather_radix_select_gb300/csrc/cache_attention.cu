@@ -21,6 +21,7 @@
 //
 // Few rows over long contexts are split into parts of the positions, whose sums and accumulators a
 // second kernel joins in a fixed order.
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 
@@ -40,6 +41,7 @@ constexpr int kUnitWarp = kMmaWarp + 1;    // the one that looks up what is next
 constexpr int kLoadWarp0 = kSoftWarps + 4;
 constexpr int kMaxRing = 5;
 constexpr int kValidSlots = 16;            // tiles whose validity bits are kept (more than the ring holds)
+constexpr int kUnits = 4;                  // units looked up ahead
 constexpr int kMaxSplit = 64;
 // A column's reference is set 2^kHeadroom above its largest weight so far and moves when a weight reaches
 // twice the reference.  bf16 has the range of fp32, so the small weights lose nothing by it, and that
@@ -52,8 +54,7 @@ constexpr int32_t kTimeout = 5;            // SEL_ETIMEOUT
 // C chunks of 128 elements a row, N columns.  Measured tensor rates: 128 x 64 x 16 takes 48.7 cycles
 // (66% of the peak: reading the operands from shared memory bounds it), 128 x 128 x 16 takes 64.6 (99%).
 // So 128 columns are taken where queries, P and two tiles of rows fit beside one another: rows of up to 192
-// elements.  (64-position tiles, two of which fit for rows of 512 elements, take 45.4 for 64 x 64 x 16, and
-// were measured slower: 716 against 532 us for 4096 rows of 64 heads over 512 selected positions.)
+// elements.
 template <int C, int N, bool FP8>
 struct Cfg {
     static_assert(N == 64 || N == 128, "");
@@ -99,13 +100,13 @@ struct Unit {
 
 struct Misc {
     uint64_t full[kMaxRing], empty[kMaxRing], s_full[2], s_empty[2], p_full[2], pv_done[2], q_full, q_empty;
-    uint64_t unit_full[2], unit_empty[2];
+    uint64_t unit_full[kUnits], unit_empty[kUnits];
     uint32_t tmem;
     int abort;
     alignas(16) float inv[kMaxCols];      // 1 / sum
     alignas(16) float part[4][kMaxCols];  // maxima, then sums, of the four warps of a group
     alignas(16) uint32_t valid[kValidSlots][4];  // bit k of word w: position 32 w + k of the tile has a cache row
-    alignas(16) Unit unit[2];
+    alignas(16) Unit unit[kUnits];
 };
 
 struct Plan {
@@ -173,14 +174,12 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-// The position in entry j of a row's list, or -1 when it stands for none.
-__device__ __forceinline__ int64_t listed(const CacheAttnArgs &a, int64_t row, int64_t j, int64_t end, int64_t cap)
+// Entry j of a row's list.
+__device__ __forceinline__ int64_t entry(const CacheAttnArgs &a, int64_t row, int64_t j)
 {
     const int64_t off = row * a.idx_row_stride + j;
-    const int64_t p = a.idx_i64 ? static_cast<const int64_t *>(a.idx)[off]
-                                : static_cast<int64_t>(static_cast<const int32_t *>(a.idx)[off]);
-    if (p >= cap && a.err_flag) atomicCAS(a.err_flag, 0, kCacheInval);
-    return p < end ? p : -1;
+    return a.idx_i64 ? __ldg(static_cast<const int64_t *>(a.idx) + off)
+                     : static_cast<int64_t>(__ldg(static_cast<const int32_t *>(a.idx) + off));
 }
 
 // One warp: unit u of the call.
@@ -188,13 +187,14 @@ template <int N, int M>
 __device__ __forceinline__ void make_unit(const Kargs &k, int64_t u, Unit *w, int lane)
 {
     const int64_t cap = k.a.t.max_pages * k.a.c.page_size;
-    // the last rows first: in a causal chunk they have the most positions
-    const int64_t item = k.p.items - 1 - u / k.p.parts;
-    const int part = static_cast<int>(u % k.p.parts);
-    const int64_t tile = item / k.p.head_blocks;
-    const int hb = static_cast<int>(item - tile * k.p.head_blocks);
-    const int64_t seq = tile / k.p.tiles_per_seq;
-    const int64_t in_seq = (tile - seq * k.p.tiles_per_seq) * k.p.rows_per_tile;
+    // the last rows first: in a causal chunk they have the most positions (32-bit divisions: no call has 2^31
+    // units)
+    const uint32_t item = static_cast<uint32_t>(k.p.items) - 1 - static_cast<uint32_t>(u) / static_cast<uint32_t>(k.p.parts);
+    const int part = static_cast<int>(static_cast<uint32_t>(u) % static_cast<uint32_t>(k.p.parts));
+    const uint32_t tile = item / static_cast<uint32_t>(k.p.head_blocks);
+    const int hb = static_cast<int>(item - tile * static_cast<uint32_t>(k.p.head_blocks));
+    const uint32_t seq = tile / static_cast<uint32_t>(k.p.tiles_per_seq);
+    const int64_t in_seq = static_cast<int64_t>(tile - seq * static_cast<uint32_t>(k.p.tiles_per_seq)) * k.p.rows_per_tile;
     const int64_t row0 = seq * k.a.t.rows_per_seq + in_seq;
     const int64_t left = k.a.t.rows_per_seq - in_seq;
     const int rows = static_cast<int>(left < k.p.rows_per_tile ? left : k.p.rows_per_tile);
@@ -220,9 +220,22 @@ __device__ __forceinline__ void make_unit(const Kargs &k, int64_t u, Unit *w, in
     int64_t keys = most;
     if (k.a.idx) {  // one row: its list up to the last entry that counts
         int last = 0;
-#pragma unroll 4
-        for (int j = lane; j < k.a.n; j += 32)
-            if (listed(k.a, row0, j, most, cap) >= 0) last = j + 1;
+        // (from the back: the last entries of most lists count)
+        auto counts = [&](int64_t p) {
+            if (p >= cap && k.a.err_flag) atomicCAS(k.a.err_flag, 0, kCacheInval);
+            return p >= 0 && p < most;
+        };
+        for (int hi = k.a.n; hi > 0 && !__any_sync(0xffffffffu, last > 0); hi -= 128) {
+            int64_t p[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int j = hi - 128 + i * 32 + lane;
+                p[i] = j >= 0 ? entry(k.a, row0, j) : -1;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (counts(p[i])) last = hi - 128 + i * 32 + lane + 1;
+        }
         keys = __reduce_max_sync(0xffffffffu, last);
     }
     if (lane == 0) {
@@ -305,23 +318,39 @@ struct Loader {
     struct Rows {
         int64_t row, scale;  // element offsets of the lane's position; row -1: none
     };
+    struct Place {
+        int page, in_page;  // kNone: no position
+    };
+    static constexpr int kNone = -0x7fffffff - 1;
 
-    // Of tile i of the unit.
-    __device__ __forceinline__ Rows find(int i) const
+    // The lane's row of a tile in three steps, taken a tile apart so that nothing waits for their loads:
+    // the position (of tile i of the unit; -1: none), its page, its row.
+    __device__ __forceinline__ int64_t position(int i) const
     {
-        Rows r{-1, 0};
         const int64_t j = static_cast<int64_t>(w->lo + i) * F::M + lw * kPos + (lane & (kPos - 1));
-        if (i >= w->n || j >= w->keys) return r;
-        const int64_t pos = k.a.idx ? listed(k.a, w->row0, j, w->list_end, k.a.t.max_pages * k.a.c.page_size) : j;
-        if (pos < 0) return r;
-        int64_t page, place;
-        if (find_row(k.a.c, k.a.t, w->seq, pos, page, place)) {
-            r.row = page * k.a.c.page_stride + place * k.a.c.row_stride;
-            r.scale = page * k.a.c.scale_page_stride + place * k.a.c.scale_row_stride;
-        } else if (k.a.err_flag) {
-            atomicCAS(k.a.err_flag, 0, kCacheInval);
+        if (i >= w->n || j >= w->keys) return -1;
+        return k.a.idx ? entry(k.a, w->row0, j) : j;
+    }
+    __device__ __forceinline__ Place page_of(int64_t pos) const
+    {
+        if (pos < 0) return Place{kNone, 0};
+        if (pos >= w->list_end) {
+            if (k.a.err_flag && pos >= k.a.t.max_pages * k.a.c.page_size) atomicCAS(k.a.err_flag, 0, kCacheInval);
+            return Place{kNone, 0};
         }
-        return r;
+        // (positions are below 2^31, and so is the size of a page where there is a page table)
+        const uint32_t p = static_cast<uint32_t>(pos), ps = static_cast<uint32_t>(k.a.c.page_size), col = p / ps;
+        return Place{__ldg(k.a.t.table + w->seq * k.a.t.stride + col), static_cast<int>(p - col * ps)};
+    }
+    __device__ __forceinline__ Rows row_of(Place at) const
+    {
+        if (at.page == kNone) return Rows{-1, 0};
+        if (at.page < 0 || at.page >= k.a.c.pages) {
+            if (k.a.err_flag) atomicCAS(k.a.err_flag, 0, kCacheInval);
+            return Rows{-1, 0};
+        }
+        return Rows{at.page * k.a.c.page_stride + at.in_page * k.a.c.row_stride,
+                    at.page * k.a.c.scale_page_stride + at.in_page * k.a.c.scale_row_stride};
     }
 
     // This warp's validity bits of the next tile.
@@ -355,11 +384,13 @@ struct Loader {
         const uint32_t to = smem_addr(smem) + (vec >> 3) * F::half_bytes + line0 * 128;
         const int halves = (d + 63) >> 6;
         constexpr int V = kVecs < 8 ? kVecs : 8;
-        Rows next = find(0);
+        int64_t pos = position(1);
+        Place at = page_of(position(0));
         for (int it = 0; it < n; ++it) {
-            const Rows cur = next;
+            const Rows cur = row_of(at);
             note(cur);
-            next = find(it + 1);
+            at = page_of(pos);
+            pos = position(it + 2);
             int64_t row[V];
             if (kVecs <= 8) {
 #pragma unroll
@@ -385,48 +416,52 @@ struct Loader {
         }
     }
 
-    // ---- 8-bit rows: loaded to registers some groups ahead, decoded to bf16 on the way to shared memory.
-    static constexpr int kLoads = !FP8 ? 1 : (kVecs < 4 ? kVecs : 4);  // 16-byte loads of a group
-    static constexpr int kGroups = FP8 ? kVecs / kLoads : 1;           // groups of a chunk
-    static constexpr int kAhead = 8 / kLoads;                          // groups in registers
-    struct Codes {
-        uint4 codes[kLoads];
-        float scale[kLoads];
+    // ---- by way of registers: loaded some groups ahead, stored (8-bit rows: decoded to bf16) when there is
+    // room.
+    static constexpr int kLoads = kVecs < 4 ? kVecs : 4;      // 16-byte loads of a group
+    static constexpr int kGroups = (kVecs + kLoads - 1) / kLoads;  // groups of a chunk
+    static constexpr int kAhead = 2;                          // groups in registers
+    struct Held {
+        uint4 v[kLoads];
+        float scale[FP8 ? kLoads : 1];
     };
 
-    __device__ __forceinline__ void rows_codes()
+    __device__ __forceinline__ void rows_held()
     {
-        const uint8_t *data = static_cast<const uint8_t *>(k.a.c.data);
-        const float *scales = k.a.c.scales;
-        const int vec = lane & 7, d = k.a.d;
+        constexpr int kElem = FP8 ? 16 : 8;  // elements of a vector
+        const int vec = lane & (kLanes - 1), d = k.a.d;
         const int total = w->n * C * kGroups;
-        Rows next = find(0);
-        const uint8_t *from[kVecs];
-        const float *by[kVecs];
+        int64_t pos = position(1);
+        Place at = page_of(position(0));
+        const unsigned char *from[kVecs];  // null: no row
+        const float *by[FP8 ? kVecs : 1];
         int fetched = 0, fg = 0, fc = 0, ft = 0;  // next group to fetch: its number in the chunk, chunk and tile
-        auto fetch = [&](Codes &x) {
+        auto fetch = [&](Held &x) {
             if (fetched >= total) return;
             if (fc == 0 && fg == 0) {
-                note(next);
+                const Rows cur = row_of(at);
+                note(cur);
+                at = page_of(pos);
+                pos = position(ft + 2);
 #pragma unroll
                 for (int i = 0; i < kVecs; ++i) {
-                    const int64_t row = __shfl_sync(0xffffffffu, next.row, 4 * i + (lane >> 3));
-                    const int64_t srow = __shfl_sync(0xffffffffu, next.scale, 4 * i + (lane >> 3));
-                    from[i] = row < 0 ? nullptr : data + row + vec * 16;
-                    by[i] = scales + srow;
+                    const int src = (32 / kLanes) * i + lane / kLanes;
+                    const int64_t row = __shfl_sync(0xffffffffu, cur.row, src);
+                    from[i] = row < 0 ? nullptr
+                                      : static_cast<const unsigned char *>(k.a.c.data) + row * (FP8 ? 1 : 2) + vec * 16;
+                    if (FP8) by[i] = k.a.c.scales + __shfl_sync(0xffffffffu, cur.scale, src);
                 }
-                next = find(ft + 1);
             }
-            const bool in = fc * 128 + vec * 16 < d;
+            const bool in = fc * 128 + vec * kElem < d;
 #pragma unroll
             for (int i = 0; i < kLoads; ++i) {
-                const uint8_t *f = kGroups == 1 || fg == 0 ? from[i] : from[kVecs - kLoads + i];
-                const float *s = kGroups == 1 || fg == 0 ? by[i] : by[kVecs - kLoads + i];
-                x.codes[i] = make_uint4(0u, 0u, 0u, 0u);
-                x.scale[i] = 1.0f;
+                const int late = kVecs - kLoads + i;
+                const unsigned char *f = kGroups == 1 || fg == 0 ? from[i] : from[late];
+                x.v[i] = make_uint4(0u, 0u, 0u, 0u);
+                if (FP8) x.scale[i] = 1.0f;
                 if (in && f) {
-                    x.codes[i] = __ldg(reinterpret_cast<const uint4 *>(f + fc * 128));
-                    x.scale[i] = __ldg(s + fc);
+                    x.v[i] = __ldg(reinterpret_cast<const uint4 *>(f + fc * (FP8 ? 128 : 256)));
+                    if (FP8) x.scale[i] = __ldg((kGroups == 1 || fg == 0 ? by[FP8 ? i : 0] : by[FP8 ? late : 0]) + fc);
                 }
             }
             ++fetched;
@@ -436,47 +471,55 @@ struct Loader {
             }
         };
         static_assert(kGroups <= 2, "");
-        const int line0 = lw * kPos + (lane >> 3);
-        const int u = (2 * vec) & 7;
-        const bool odd = vec >= 4;
-        unsigned char *to = smem + (vec >> 2) * F::half_bytes + line0 * 128;
-        // 16 values of a line: units u, u + 1.  Lanes of the second half store their second unit first: the 8
+        constexpr int kStep = 32 / kLanes;  // lines between a lane's vectors
+        const int line0 = lw * kPos + lane / kLanes;
+        const int u = FP8 ? (2 * vec) & 7 : vec & 7, half = FP8 ? vec >> 2 : vec >> 3;
+        const bool odd = FP8 && vec >= 4;
+        unsigned char *to = smem + half * F::half_bytes + line0 * 128;
+        // 16 codes of a line: units u, u + 1.  Lanes of the second half store their second unit first: the 8
         // lanes of a line then cover all banks in each of the two stores.
-        auto put = [&](unsigned char *at, int sw, uint4 a, uint4 b) {
-            *reinterpret_cast<uint4 *>(at + (((u + odd) ^ sw) << 4)) = odd ? b : a;
-            *reinterpret_cast<uint4 *>(at + (((u + !odd) ^ sw) << 4)) = odd ? a : b;
+        auto put = [&](unsigned char *at_line, int sw, uint4 a, uint4 b) {
+            *reinterpret_cast<uint4 *>(at_line + (((u + odd) ^ sw) << 4)) = odd ? b : a;
+            *reinterpret_cast<uint4 *>(at_line + (((u + !odd) ^ sw) << 4)) = odd ? a : b;
         };
         int sg = 0;  // group of the chunk being stored
-        auto store = [&](int g, const Codes &x) {
+        auto store = [&](int g, const Held &x) {
             if (g >= total) return;
             if (sg == 0) wait(&m->empty[stage], phase);
-            unsigned char *base = to + stage * F::chunk_bytes + sg * (kLoads * 4 * 128);
-            bool fast = true;
+            unsigned char *base = to + stage * F::chunk_bytes + sg * (kLoads * kStep * 128);
+            if (!FP8) {
 #pragma unroll
-            for (int i = 0; i < kLoads; ++i) fast &= decodes_fast(x.codes[i], x.scale[i]);
-            if (fast) {
-#pragma unroll
-                for (int i = 0; i < kLoads; ++i) {
-                    const uint32_t f = (__float_as_uint(x.scale[i]) >> 16) + (120u << 7), by2 = f | (f << 16);
-                    const uint2 a0 = decode4_fast(x.codes[i].x, by2), a1 = decode4_fast(x.codes[i].y, by2);
-                    const uint2 b0 = decode4_fast(x.codes[i].z, by2), b1 = decode4_fast(x.codes[i].w, by2);
-                    put(base + i * 512, (line0 + 4 * i) & 7, make_uint4(a0.x, a0.y, a1.x, a1.y),
-                        make_uint4(b0.x, b0.y, b1.x, b1.y));
-                }
+                for (int i = 0; i < kLoads; ++i)
+                    *reinterpret_cast<uint4 *>(base + i * (kStep * 128) +
+                                               ((u ^ ((line0 + kStep * (sg * kLoads + i)) & 7)) << 4)) = x.v[i];
             } else {
-#pragma unroll 1
-                for (int i = 0; i < kLoads; ++i) {
-                    uint4 c = x.codes[0];
-                    float f = x.scale[0];
+                bool fast = true;
 #pragma unroll
-                    for (int j = 1; j < kLoads; ++j) {
-                        c = i == j ? x.codes[j] : c;
-                        f = i == j ? x.scale[j] : f;
+                for (int i = 0; i < kLoads; ++i) fast &= decodes_fast(x.v[i], x.scale[FP8 ? i : 0]);
+                if (fast) {
+#pragma unroll
+                    for (int i = 0; i < kLoads; ++i) {
+                        const uint32_t f = (__float_as_uint(x.scale[FP8 ? i : 0]) >> 16) + (120u << 7), by2 = f | (f << 16);
+                        const uint2 a0 = decode4_fast(x.v[i].x, by2), a1 = decode4_fast(x.v[i].y, by2);
+                        const uint2 b0 = decode4_fast(x.v[i].z, by2), b1 = decode4_fast(x.v[i].w, by2);
+                        put(base + i * (kStep * 128), (line0 + kStep * i) & 7, make_uint4(a0.x, a0.y, a1.x, a1.y),
+                            make_uint4(b0.x, b0.y, b1.x, b1.y));
                     }
-                    const uint2 a0 = decode4_exact(c.x, f), a1 = decode4_exact(c.y, f);
-                    const uint2 b0 = decode4_exact(c.z, f), b1 = decode4_exact(c.w, f);
-                    put(base + i * 512, (line0 + 4 * i) & 7, make_uint4(a0.x, a0.y, a1.x, a1.y),
-                        make_uint4(b0.x, b0.y, b1.x, b1.y));
+                } else {
+#pragma unroll 1
+                    for (int i = 0; i < kLoads; ++i) {
+                        uint4 c = x.v[0];
+                        float f = x.scale[0];
+#pragma unroll
+                        for (int j = 1; j < kLoads; ++j) {
+                            c = i == j ? x.v[j] : c;
+                            f = i == j ? x.scale[FP8 ? j : 0] : f;
+                        }
+                        const uint2 a0 = decode4_exact(c.x, f), a1 = decode4_exact(c.y, f);
+                        const uint2 b0 = decode4_exact(c.z, f), b1 = decode4_exact(c.w, f);
+                        put(base + i * (kStep * 128), (line0 + kStep * i) & 7, make_uint4(a0.x, a0.y, a1.x, a1.y),
+                            make_uint4(b0.x, b0.y, b1.x, b1.y));
+                    }
                 }
             }
             if (++sg < kGroups) return;
@@ -486,7 +529,7 @@ struct Loader {
             if (lane == 0) mbar_arrive(&m->full[stage]);
             next_stage();
         };
-        Codes x[kAhead];
+        Held x[kAhead];
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) fetch(x[i]);
         for (int g = 0; g < total; g += kAhead) {
@@ -718,8 +761,9 @@ struct Softmax {
 
     // A tile's weights 2^(score * scale - reference), two positions by G pairs of columns a block, as bf16
     // pairs; added to `to`.  Returns whether one is 2 or more (or NaN).
-    __device__ __forceinline__ bool weights(const float x[H][X], const Mask &mask, bool whole, uint32_t dirty,
-                                            uint32_t out[H][2 * G], float2 to[G]) const
+    template <bool WHOLE>
+    __device__ __forceinline__ bool weights_of(const float x[H][X], const Mask &mask, uint32_t dirty,
+                                               uint32_t out[H][2 * G], float2 to[G]) const
     {
         const float2 scale = make_float2(k.a.scale_log2, k.a.scale_log2);
         uint32_t any = 0;
@@ -731,7 +775,7 @@ struct Softmax {
                 for (int r = 0; r < 2; ++r) {
                     const int i = 4 * g + 2 * r;
                     float2 y = fma2(make_float2(x[h][i], x[h][i + 1]), scale, neg[g]);
-                    if (!whole) {
+                    if (!WHOLE) {
                         // (a column without positions has no finite reference: its scores are all masked)
                         y.x = masked(mask, y.x, h, i);
                         y.y = masked(mask, y.y, h, i + 1);
@@ -746,6 +790,12 @@ struct Softmax {
                     any |= out[h][2 * g + r];
                 }
         return (any & 0x40004000u) != 0;
+    }
+    __device__ __forceinline__ bool weights(const float x[H][X], const Mask &mask, bool whole, uint32_t dirty,
+                                            uint32_t out[H][2 * G], float2 to[G]) const
+    {
+        // (one branch, not one an element: the exponentials of a thread then overlap)
+        return whole ? weights_of<true>(x, mask, dirty, out, to) : weights_of<false>(x, mask, dirty, out, to);
     }
 
     // A position that one row attends to and another does not has weight 0 in the other, but 0 * NaN is
@@ -967,6 +1017,8 @@ __global__ void __launch_bounds__(Cfg<C, N, FP8>::threads, 1) attention_kernel(c
             mbar_init(&m->s_empty[i], kSoftWarps);
             mbar_init(&m->p_full[i], kSoftWarps);
             mbar_init(&m->pv_done[i], 1);
+        }
+        for (int i = 0; i < kUnits; ++i) {
             mbar_init(&m->unit_full[i], 1);
             mbar_init(&m->unit_empty[i], kSoftWarps + 3 + F::load_warps);
         }
@@ -980,14 +1032,14 @@ __global__ void __launch_bounds__(Cfg<C, N, FP8>::threads, 1) attention_kernel(c
     __syncthreads();
     tmem_fence_after();
     const Waiter wait{&m->abort, k.a.err_flag};
-    // unit i of this CTA is in slot i mod 2
+    // unit i of this CTA is in slot i mod kUnits
     auto take = [&](int i) -> const Unit * {
-        wait(&m->unit_full[i & 1], (i >> 1) & 1);
-        return &m->unit[i & 1];
+        wait(&m->unit_full[i % kUnits], (i / kUnits) & 1);
+        return &m->unit[i % kUnits];
     };
     auto give = [&](int i) {
         __syncwarp();
-        if (lane == 0) mbar_arrive(&m->unit_empty[i & 1]);
+        if (lane == 0) mbar_arrive(&m->unit_empty[i % kUnits]);
     };
 
     if (warp < kSoftWarps) {
@@ -1022,10 +1074,10 @@ __global__ void __launch_bounds__(Cfg<C, N, FP8>::threads, 1) attention_kernel(c
         } else if (warp == kUnitWarp) {
             int i = 0;
             for (int64_t u = blockIdx.x; u < units; u += gridDim.x, ++i) {
-                wait(&m->unit_empty[i & 1], ((i >> 1) & 1) ^ 1);
-                make_unit<N, F::M>(k, u, &m->unit[i & 1], lane);
+                wait(&m->unit_empty[i % kUnits], ((i / kUnits) & 1) ^ 1);
+                make_unit<N, F::M>(k, u, &m->unit[i % kUnits], lane);
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&m->unit_full[i & 1]);
+                if (lane == 0) mbar_arrive(&m->unit_full[i % kUnits]);
             }
         } else {
             int i = 0, loaded = 0;
@@ -1046,7 +1098,7 @@ __global__ void __launch_bounds__(Cfg<C, N, FP8>::threads, 1) attention_kernel(c
             load.w = take(i);
             if (load.w->n > 0) {
                 if (FP8)
-                    load.rows_codes();
+                    load.rows_held();
                 else
                     load.rows_bf16();
             }
@@ -1062,6 +1114,7 @@ __global__ void __launch_bounds__(Cfg<C, N, FP8>::threads, 1) attention_kernel(c
 // Joins the parts of each (row, head): out = sum_p 2^(ref_p - max) o_p / sum_p 2^(ref_p - max) sum_p.
 __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Kargs k)
 {
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // launched ahead: until the parts are there
     const int64_t item = blockIdx.x;
     const int parts = k.p.parts, dv = k.a.dv;
     const float2 *ml = k.part_ml + item * parts;
@@ -1090,6 +1143,18 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Kargs
     if (threadIdx.x == 0 && k.a.lse) k.a.lse[item] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
 }
 
+// The current device's SMs, asked for once a device.
+int sm_count()
+{
+    static std::atomic<int> known[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    if (dev >= 64) return device_sm_count();
+    int n = known[dev].load(std::memory_order_relaxed);
+    if (n == 0) known[dev].store(n = device_sm_count(), std::memory_order_relaxed);
+    return n;
+}
+
 template <int C, int N, bool FP8>
 cudaError_t launch(const Kargs &k, cudaStream_t s)
 {
@@ -1098,10 +1163,19 @@ cudaError_t launch(const Kargs &k, cudaStream_t s)
     static_assert(smem <= 232448, "more than a CTA may use");
     static_assert(smem > 116 * 1024, "one CTA an SM: each takes all of the tensor memory");
     static_assert(4 * F::cols_per_group * 256 <= F::pbufs * F::p_bytes, "outputs are staged where P was");
-    cudaError_t e = cudaFuncSetAttribute(attention_kernel<C, N, FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(smem));
+    // the attribute is set once on each device (a device past the mask's 64: on each call)
+    static std::atomic<uint64_t> set{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    const int64_t units = k.p.items * k.p.parts, sms = device_sm_count();
+    const uint64_t bit = dev < 64 ? uint64_t{1} << dev : 0;
+    if (!(set.load(std::memory_order_relaxed) & bit)) {
+        e = cudaFuncSetAttribute(attention_kernel<C, N, FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 static_cast<int>(smem));
+        if (e != cudaSuccess) return e;
+        set.fetch_or(bit, std::memory_order_relaxed);
+    }
+    const int64_t units = k.p.items * k.p.parts, sms = sm_count();
     attention_kernel<C, N, FP8><<<static_cast<unsigned>(units < sms ? units : sms), F::threads, smem, s>>>(k);
     return cudaGetLastError();
 }
@@ -1128,7 +1202,7 @@ Plan plan_of(int64_t rows, int64_t h, int64_t d, int64_t b, int64_t positions, b
     p.items = b * p.tiles_per_seq * p.head_blocks;
     // parts: as many as keep the fewest tiles in a row, counting a part's start and end as 1.5 tiles
     const int64_t tiles = (positions + 127) / 128;
-    const int64_t sms = device_sm_count() > 0 ? device_sm_count() : 1;
+        const int64_t sms = sm_count() > 0 ? sm_count() : 1;
     p.parts = 1;
     double best = 0.0;
     for (int64_t n = 1; n <= kMaxSplit && n <= (tiles > 1 ? tiles : 1); ++n) {
@@ -1172,8 +1246,16 @@ cudaError_t launch_cache_attention(const CacheAttnArgs &a, cudaStream_t s)
     else
         e = a.d <= 384 ? launch<3, 64>(k, s) : launch<4, 64>(k, s);
     if (e != cudaSuccess || k.p.parts == 1) return e;
-    join_kernel<<<static_cast<unsigned>(a.rows * a.h), 128, 0, s>>>(k);
-    return cudaGetLastError();
+    cudaLaunchConfig_t at = {};
+    at.gridDim = dim3(static_cast<unsigned>(a.rows * a.h));
+    at.blockDim = dim3(128);
+    at.stream = s;
+    cudaLaunchAttribute ahead;
+    ahead.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    ahead.val.programmaticStreamSerializationAllowed = 1;
+    at.attrs = &ahead;
+    at.numAttrs = 1;
+    return cudaLaunchKernelEx(&at, join_kernel, k);
 }
 
 }  // namespace sel

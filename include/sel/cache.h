@@ -63,7 +63,8 @@ typedef struct {
  * SEL_BF16: fp32 rows are rounded to nearest even.  SEL_E4M3: each run of 128
  * gets the smallest power of two 2^e, e >= -126, with 448 * 2^e >= its largest
  * finite magnitude, and the codes are value / 2^e rounded to nearest even; an
- * infinity is stored as +-448 * 2^e, a NaN as NaN. */
+ * infinity is stored as +-448 * 2^e, a NaN as NaN.
+ * SEL_EUNSUPPORTED: tokens * ceil(d / SEL_CACHE_GROUP) >= 2^27. */
 SEL_API int sel_cache_write(const void *x, int x_dtype, int64_t tokens, int64_t x_stride, const void *slots,
                             int slot_dtype, const sel_cache *cache, int32_t *err_flag, void *stream);
 
