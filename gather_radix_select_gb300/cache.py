@@ -11,7 +11,7 @@ call belongs to sequence ``r // (rows // b)``.
 """
 from __future__ import annotations
 
-import ctypes
+import functools
 import math
 
 import torch
@@ -102,6 +102,28 @@ def _launch(dev, stream, call):
         return call(torch._C._cuda_getCurrentRawStream(index))
     with torch.cuda.device(dev):
         return call(torch._C._cuda_getCurrentRawStream(index))
+
+
+@functools.lru_cache(maxsize=4096)
+def _scratch_bytes(device_index, rows, h, d, dv, b, max_pages, page_size, idx_given, n):
+    """Scratch that a call of this shape needs on the (current) device."""
+    return int(_native.load().sel_cache_attention_workspace_size(rows, h, d, dv, b, max_pages, page_size, idx_given,
+                                                                 n))
+
+
+_SCRATCH: dict = {}
+
+
+def _scratch(nbytes, like, raw_stream):
+    """A scratch buffer of >= nbytes kept for each stream (calls on one stream never overlap), or, while a graph is
+    captured, one of its own."""
+    if torch.cuda.is_current_stream_capturing():
+        return like.new_empty(nbytes, dtype=torch.uint8)
+    key = (like.device.index, raw_stream)
+    buf = _SCRATCH.get(key)
+    if buf is None or buf.shape[0] < nbytes:
+        buf = _SCRATCH[key] = like.new_empty(max(nbytes, 1 << 20), dtype=torch.uint8)
+    return buf
 
 
 def cache_write(x: torch.Tensor, cache: torch.Tensor, slots: torch.Tensor, *, scales: torch.Tensor | None = None,
@@ -211,8 +233,8 @@ def cache_attention(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tens
         lib = _native.load()
         to = q.new_empty((rows, h, max(dv, 0))) if out is None else out
         lse = q.new_empty((rows, h), dtype=torch.float32) if return_lse else None
-        need = lib.sel_cache_attention_workspace_size(rows, h, d, dv, b, m, c.page_size, idx_ptr is not None, n)
-        ws = q.new_empty(need, dtype=torch.uint8) if need else None
+        need = _scratch_bytes(dev.index, rows, h, d, dv, b, m, c.page_size, idx_ptr is not None, n)
+        ws = _scratch(need, q, s) if need else None
         return lib.sel_cache_attention(
             q.data_ptr(), rows, h, q_row if rows > 1 else h * d, q_head if h > 1 else d, c, page_table.data_ptr(),
             b, m, table_stride, None if end is None else end.data_ptr(), idx_ptr, idx_type, n, idx_stride, dv,

@@ -95,6 +95,7 @@ struct Unit {
     int min_end, max_end;    // of its rows
     alignas(16) int end[kMaxCols];  // exclusive end of each column's row, 0 for unused columns
     alignas(16) int out[kMaxCols];  // row * heads + head of each column
+    alignas(16) int64_t q[kMaxCols];  // element offset of each column's query, -1 for unused columns
     __device__ __forceinline__ int cols() const { return rows * heads; }
 };
 
@@ -206,7 +207,9 @@ __device__ __forceinline__ void make_unit(const Kargs &k, int64_t u, Unit *w, in
         const int col = i * 32 + lane;
         int e = 0;
         const int row = col / heads;
-        w->out[col] = static_cast<int>((row0 + row) * k.a.h) + head0 + col - row * heads;
+        const int head = head0 + col - row * heads;
+        w->out[col] = static_cast<int>((row0 + row) * k.a.h) + head;
+        w->q[col] = col < rows * heads ? (row0 + row) * k.a.q_row_stride + head * k.a.q_head_stride : -1;
         if (col < rows * heads) {
             const int64_t v = k.a.end ? k.a.end[row0 + row] : cap;
             e = static_cast<int>(v < 0 ? 0 : (v > cap ? cap : v));
@@ -547,21 +550,19 @@ template <int C, int N, bool FP8>
 __device__ __forceinline__ void load_queries(const Kargs &k, const Unit *w, Misc *m, unsigned char *smem, int warp, int lane)
 {
     using F = Cfg<C, N, FP8>;
-    const int vec = lane & 15, heads = w->heads, cols = w->cols();
+    const int vec = lane & 15;
     const uint32_t to = smem_addr(smem + F::q_off) + (vec >> 3) * F::q_half;
 #pragma unroll 4
     for (int i = 0; i < N / 4; ++i) {
         const int col = (i * 2 + warp) * 2 + (lane >> 4);
-        const int row = col / heads;
-        const uint16_t *src = k.a.q + (w->row0 + row) * k.a.q_row_stride +
-                              static_cast<int64_t>(w->head0 + col - row * heads) * k.a.q_head_stride;
+        const int64_t at = w->q[col];
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             const int e = c * 128 + vec * 8;
-            const bool ok = col < cols && e < k.a.d;
+            const bool ok = at >= 0 && e < k.a.d;
             if (c * 2 + (vec >> 3) < F::q_halves)
-                cp_async16(to + c * 2 * F::q_half + col * 128 + (((vec & 7) ^ (col & 7)) << 4), ok ? src + e : k.a.q,
-                           ok ? 16u : 0u);
+                cp_async16(to + c * 2 * F::q_half + col * 128 + (((vec & 7) ^ (col & 7)) << 4),
+                           k.a.q + (ok ? at + e : 0), ok ? 16u : 0u);
         }
     }
     cp_async_wait_all();
