@@ -196,7 +196,8 @@ int sel_cache_attention(const void *q, int64_t rows, int64_t h, int64_t q_row_st
     a.idx_i64 = idx_dtype == SEL_I64;
     a.n = idx ? static_cast<int32_t>(n) : 0;
     a.idx_row_stride = idx_row_stride;
-    a.scale_log2 = scale * kLog2e;
+    // (a scale of 0 becomes the smallest number, so that a masked score, an infinity, keeps the weight 0)
+    a.scale_log2 = scale == 0.0f ? 1.4e-45f : scale * kLog2e;
     a.out = static_cast<uint16_t *>(out);
     a.lse = lse;
     a.err_flag = err_flag;

@@ -35,10 +35,6 @@ namespace sel {
 namespace {
 
 constexpr int kMaxCols = 128;              // (row, head) columns of a CTA at most
-constexpr int kSoftWarps = 16;             // four groups of 4 warps, a quarter of the columns each
-constexpr int kMmaWarp = kSoftWarps;       // the one that issues, in a group of 4 with
-constexpr int kUnitWarp = kMmaWarp + 1;    // the one that looks up what is next and two that stage queries
-constexpr int kLoadWarp0 = kSoftWarps + 4;
 constexpr int kMaxRing = 5;
 constexpr int kValidSlots = 16;            // tiles whose validity bits are kept (more than the ring holds)
 constexpr int kUnits = 4;                  // units looked up ahead
@@ -72,16 +68,24 @@ struct Cfg {
     static constexpr int q_off = ring * chunk_bytes;
     static constexpr int p_off = q_off + q_halves * q_half;
     static constexpr int misc_off = p_off + pbufs * p_bytes;
-    static constexpr int cols_per_group = N / 4;
-    static constexpr int load_warps = wide && FP8 ? 4 : 8;
-    static constexpr int threads = (kLoadWarp0 + load_warps) * 32;
+    // Warps: groups of 4 for the softmax, an equal share of the columns each; a group of 4 with the one that
+    // issues, the one that looks up what is next and two that stage queries; those that stage rows.
+    // 8-bit rows take two sets of the last, which stage every other chunk each, and fewer of the first: the
+    // time from a load to the decoded chunk bounds them.
+    static constexpr int groups = FP8 && !wide ? 2 : 4;
+    static constexpr int cols_per_group = N / groups;
+    static constexpr int soft_warps = 4 * groups, mma_warp = soft_warps, unit_warp = soft_warps + 1;
+    static constexpr int load_warp0 = soft_warps + 4;
+    static constexpr int load_sets = FP8 && !wide ? 2 : 1, set_warps = wide && FP8 ? 4 : 8;
+    static constexpr int load_warps = load_sets * set_warps;
+    static constexpr int threads = (load_warp0 + load_warps) * 32;
     // Registers a thread after the roles part, of 896 x 72 (768 x 80) at the launch.
     static constexpr int launch_regs = load_warps == 4 ? 80 : 72;
-    static constexpr int soft_regs = wide ? 88 : 64;
-    static constexpr int mma_regs = 40;
-    static constexpr int load_regs = load_warps == 4 ? 88 : (wide ? 48 : 96);
+    static constexpr int soft_regs = wide ? (FP8 ? 88 : 96) : FP8 ? 96 : 64;
+    static constexpr int mma_regs = wide && !FP8 ? 32 : 40;
+    static constexpr int load_regs = wide ? (FP8 ? 88 : 40) : FP8 ? 64 : 96;
     static_assert(ring >= C && ring <= kMaxRing, "");
-    static_assert(512 * soft_regs + 128 * mma_regs + 32 * load_warps * load_regs <= threads * launch_regs, "");
+    static_assert(32 * soft_warps * soft_regs + 128 * mma_regs + 32 * load_warps * load_regs <= threads * launch_regs, "");
 };
 
 // What a CTA works on next, made by one warp ahead of the others.
@@ -228,6 +232,7 @@ __device__ __forceinline__ void make_unit(const Kargs &k, int64_t u, Unit *w, in
             if (p >= cap && k.a.err_flag) atomicCAS(k.a.err_flag, 0, kCacheInval);
             return p >= 0 && p < most;
         };
+#pragma unroll 1
         for (int hi = k.a.n; hi > 0 && !__any_sync(0xffffffffu, last > 0); hi -= 128) {
             int64_t p[4];
 #pragma unroll
@@ -259,15 +264,35 @@ __device__ __forceinline__ void make_unit(const Kargs &k, int64_t u, Unit *w, in
 }
 
 // ------------------------------------------------------------------------------------ staging rows
+// Loads under a predicate, without a branch; 0 (or `other`) where it is false.
+__device__ __forceinline__ uint2 load8_if(const void *p, bool yes)
+{
+    uint2 v;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %3, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\t"
+        "@p ld.global.nc.v2.u32 {%0, %1}, [%2];\n\t}"
+        : "=&r"(v.x), "=&r"(v.y)
+        : "l"(p), "r"(yes ? 1 : 0));
+    return v;
+}
+__device__ __forceinline__ float load4_if(const float *p, bool yes, float other)
+{
+    float v;
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\tmov.b32 %0, %3;\n\t@p ld.global.nc.f32 %0, [%1];\n\t}"
+                 : "=&f"(v)
+                 : "l"(p), "r"(yes ? 1 : 0), "f"(other));
+    return v;
+}
+
 // 8-bit codes to bf16.  With a scale that is a power of two below 2^8 and no NaN among the codes
 // (decodes_fast), a code's exponent and mantissa bits, put where bf16 has them, are its value times 2^-120
 // (subnormal codes give subnormal numbers), and one bf16 product makes that value * scale, rounding only
 // where the result is subnormal.  Else by way of fp32.
-__device__ __forceinline__ bool decodes_fast(uint4 codes, float scale)
+__device__ __forceinline__ bool decodes_fast(uint2 lo, uint2 hi, float scale)
 {
     const uint32_t s = __float_as_uint(scale);
-    const uint32_t nan = ((codes.x & 0x7f7f7f7fu) + 0x01010101u) | ((codes.y & 0x7f7f7f7fu) + 0x01010101u) |
-                         ((codes.z & 0x7f7f7f7fu) + 0x01010101u) | ((codes.w & 0x7f7f7f7fu) + 0x01010101u);
+    const uint32_t nan = ((lo.x & 0x7f7f7f7fu) + 0x01010101u) | ((lo.y & 0x7f7f7f7fu) + 0x01010101u) |
+                         ((hi.x & 0x7f7f7f7fu) + 0x01010101u) | ((hi.y & 0x7f7f7f7fu) + 0x01010101u);
     return ((s & 0x007fffffu) | (nan & 0x80808080u)) == 0 && s - 0x00800000u < (134u << 23);
 }
 
@@ -306,7 +331,7 @@ struct Loader {
     using F = Cfg<C, N, FP8>;
     // Warp lw stages positions lw * kPos .. of each tile: lane mod kPos looks one up, and the lanes of a
     // line (16 of 16 bytes of bf16, 8 of 16 codes) keep the rows they copy in registers for the tile.
-    static constexpr int kPos = F::M / F::load_warps;  // 8, 16 or 32
+    static constexpr int kPos = F::M / F::set_warps;  // 16 or 32
     static constexpr int kLanes = FP8 ? 8 : 16;        // lanes of a line
     static constexpr int kVecs = kPos * kLanes / 32;   // lines a lane takes part in
     const Kargs &k;
@@ -316,7 +341,7 @@ struct Loader {
     int lane, lw;
     const Unit *w = nullptr;
     int stage = 0, phase = 1;  // of the ring; a fresh barrier's phase of parity 1 counts as completed
-    int tile = 0;              // tiles staged so far
+    int tile = 0;              // tiles staged in units before
 
     struct Rows {
         int64_t row, scale;  // element offsets of the lane's position; row -1: none
@@ -356,20 +381,17 @@ struct Loader {
                     at.page * k.a.c.scale_page_stride + at.in_page * k.a.c.scale_row_stride};
     }
 
-    // This warp's validity bits of the next tile.
-    __device__ __forceinline__ void note(const Rows &r)
+    // This warp's validity bits of tile i of the unit.
+    __device__ __forceinline__ void note(int i, const Rows &r) const
     {
         const uint32_t bits = __ballot_sync(0xffffffffu, r.row >= 0);
-        uint32_t *to = m->valid[tile & (kValidSlots - 1)];
+        uint32_t *to = m->valid[(tile + i) & (kValidSlots - 1)];
         if (lane == 0) {
             if (kPos == 32)
                 to[lw] = bits;
-            else if (kPos == 16)
-                reinterpret_cast<uint16_t *>(to)[lw] = static_cast<uint16_t>(bits);
             else
-                reinterpret_cast<uint8_t *>(to)[lw] = static_cast<uint8_t>(bits);
+                reinterpret_cast<uint16_t *>(to)[lw] = static_cast<uint16_t>(bits);
         }
-        ++tile;
     }
 
     __device__ __forceinline__ void next_stage()
@@ -389,9 +411,10 @@ struct Loader {
         constexpr int V = kVecs < 8 ? kVecs : 8;
         int64_t pos = position(1);
         Place at = page_of(position(0));
+#pragma unroll 1
         for (int it = 0; it < n; ++it) {
             const Rows cur = row_of(at);
-            note(cur);
+            note(it, cur);
             at = page_of(pos);
             pos = position(it + 2);
             int64_t row[V];
@@ -419,129 +442,119 @@ struct Loader {
         }
     }
 
-    // ---- by way of registers: loaded some groups ahead, stored (8-bit rows: decoded to bf16) when there is
-    // room.
-    static constexpr int kLoads = kVecs < 4 ? kVecs : 4;      // 16-byte loads of a group
+    // ---- 8-bit rows: loaded to registers a group ahead, decoded to bf16 on the way to shared memory.  (Two
+    // groups ahead were measured slower, 188 against 157 us for 1024 rows over 512 selected positions of 512;
+    // a second set of warps, with chunks of its own, hides the loads instead.)  A lane takes codes 8 v .. and
+    // 64 + 8 v .. of a line's 128 (v = lane mod 8): the 8 lanes of a line then store its 8 units of either half,
+    // without bank conflicts.
+    static constexpr int kLoads = kVecs < 4 ? kVecs : 4;           // lines of a group
     static constexpr int kGroups = (kVecs + kLoads - 1) / kLoads;  // groups of a chunk
-    static constexpr int kAhead = 2;                          // groups in registers
-    struct Held {
-        uint4 v[kLoads];
-        float scale[FP8 ? kLoads : 1];
+    struct Codes {
+        uint2 lo[kLoads], hi[kLoads];
+        float scale[kLoads];
     };
+    int chunks = 0;  // staged in units before, by all sets
 
-    __device__ __forceinline__ void rows_held()
+    __device__ __forceinline__ void rows_codes(int set)
     {
-        constexpr int kElem = FP8 ? 16 : 8;  // elements of a vector
-        const int vec = lane & (kLanes - 1), d = k.a.d;
-        const int total = w->n * C * kGroups;
-        int64_t pos = position(1);
-        Place at = page_of(position(0));
-        const unsigned char *from[kVecs];  // null: no row
-        const float *by[FP8 ? kVecs : 1];
-        int fetched = 0, fg = 0, fc = 0, ft = 0;  // next group to fetch: its number in the chunk, chunk and tile
-        auto fetch = [&](Held &x) {
-            if (fetched >= total) return;
-            if (fc == 0 && fg == 0) {
+        constexpr int S = F::load_sets, kNext = C < S ? S : 1;  // chunks, tiles from one of the warp's to its next
+        const uint8_t *data = static_cast<const uint8_t *>(k.a.c.data);
+        const float *scales = k.a.c.scales;
+        const int vec = lane & 7, d = k.a.d;
+        const int total = w->n * C;
+        int g = S == 1 || (chunks & 1) == set ? 0 : 1;  // the warp's next chunk of the unit
+        int fc = g % C, ft = g / C, fg = 0;             // of the next group to fetch: chunk of the tile, tile, group
+        bool fresh = true;                              // rows of tile ft not looked up yet
+        int64_t pos = position(ft + kNext);
+        Place at = page_of(position(ft));
+        const uint8_t *from[kVecs];  // null: no row
+        const float *by[kVecs];
+        auto fetch = [&](Codes &x) {
+            if (ft >= w->n) return;
+            if (fresh) {
                 const Rows cur = row_of(at);
-                note(cur);
+                if (fc == 0) note(ft, cur);
                 at = page_of(pos);
-                pos = position(ft + 2);
+                pos = position(ft + 2 * kNext);
 #pragma unroll
                 for (int i = 0; i < kVecs; ++i) {
-                    const int src = (32 / kLanes) * i + lane / kLanes;
-                    const int64_t row = __shfl_sync(0xffffffffu, cur.row, src);
-                    from[i] = row < 0 ? nullptr
-                                      : static_cast<const unsigned char *>(k.a.c.data) + row * (FP8 ? 1 : 2) + vec * 16;
-                    if (FP8) by[i] = k.a.c.scales + __shfl_sync(0xffffffffu, cur.scale, src);
+                    const int64_t row = __shfl_sync(0xffffffffu, cur.row, 4 * i + (lane >> 3));
+                    from[i] = row < 0 ? nullptr : data + row + vec * 8;
+                    by[i] = scales + __shfl_sync(0xffffffffu, cur.scale, 4 * i + (lane >> 3));
                 }
+                fresh = false;
             }
-            const bool in = fc * 128 + vec * kElem < d;
+            const bool in = fc * 128 + vec * 8 < d, in_hi = fc * 128 + 64 + vec * 8 < d;
 #pragma unroll
             for (int i = 0; i < kLoads; ++i) {
                 const int late = kVecs - kLoads + i;
-                const unsigned char *f = kGroups == 1 || fg == 0 ? from[i] : from[late];
-                x.v[i] = make_uint4(0u, 0u, 0u, 0u);
-                if (FP8) x.scale[i] = 1.0f;
-                if (in && f) {
-                    x.v[i] = __ldg(reinterpret_cast<const uint4 *>(f + fc * (FP8 ? 128 : 256)));
-                    if (FP8) x.scale[i] = __ldg((kGroups == 1 || fg == 0 ? by[FP8 ? i : 0] : by[FP8 ? late : 0]) + fc);
-                }
+                const uint8_t *f = kGroups == 1 || fg == 0 ? from[i] : from[late];
+                const float *s = kGroups == 1 || fg == 0 ? by[i] : by[late];
+                x.lo[i] = load8_if(f + fc * 128, f && in);
+                x.hi[i] = load8_if(f + fc * 128 + 64, f && in_hi);
+                x.scale[i] = load4_if(s + fc, f && in, 1.0f);
             }
-            ++fetched;
-            if (++fg == kGroups) {
-                fg = 0;
-                if (++fc == C) fc = 0, ++ft;
+            if (++fg < kGroups) return;
+            fg = 0;
+            fc += S;
+            if (fc >= C) {
+                ft += fc / C;
+                fc %= C;
+                fresh = true;
             }
         };
-        static_assert(kGroups <= 2, "");
-        constexpr int kStep = 32 / kLanes;  // lines between a lane's vectors
-        const int line0 = lw * kPos + lane / kLanes;
-        const int u = FP8 ? (2 * vec) & 7 : vec & 7, half = FP8 ? vec >> 2 : vec >> 3;
-        const bool odd = FP8 && vec >= 4;
-        unsigned char *to = smem + half * F::half_bytes + line0 * 128;
-        // 16 codes of a line: units u, u + 1.  Lanes of the second half store their second unit first: the 8
-        // lanes of a line then cover all banks in each of the two stores.
-        auto put = [&](unsigned char *at_line, int sw, uint4 a, uint4 b) {
-            *reinterpret_cast<uint4 *>(at_line + (((u + odd) ^ sw) << 4)) = odd ? b : a;
-            *reinterpret_cast<uint4 *>(at_line + (((u + !odd) ^ sw) << 4)) = odd ? a : b;
-        };
-        int sg = 0;  // group of the chunk being stored
-        auto store = [&](int g, const Held &x) {
-            if (g >= total) return;
-            if (sg == 0) wait(&m->empty[stage], phase);
-            unsigned char *base = to + stage * F::chunk_bytes + sg * (kLoads * kStep * 128);
-            if (!FP8) {
-#pragma unroll
-                for (int i = 0; i < kLoads; ++i)
-                    *reinterpret_cast<uint4 *>(base + i * (kStep * 128) +
-                                               ((u ^ ((line0 + kStep * (sg * kLoads + i)) & 7)) << 4)) = x.v[i];
-            } else {
+        static_assert(!FP8 || kGroups <= 2, "");
+        const int line0 = lw * kPos + (lane >> 3);
+        unsigned char *to = smem + line0 * 128;
+        Codes x;
+        fetch(x);
+#pragma unroll 1
+        for (; g < total; g += S) {
+            wait(&m->empty[stage], phase);
+#pragma unroll 1
+            for (int sg = 0; sg < kGroups; ++sg) {
+                unsigned char *base = to + stage * F::chunk_bytes + sg * (kLoads * 4 * 128);
                 bool fast = true;
 #pragma unroll
-                for (int i = 0; i < kLoads; ++i) fast &= decodes_fast(x.v[i], x.scale[FP8 ? i : 0]);
+                for (int i = 0; i < kLoads; ++i) fast &= decodes_fast(x.lo[i], x.hi[i], x.scale[i]);
                 if (fast) {
 #pragma unroll
                     for (int i = 0; i < kLoads; ++i) {
-                        const uint32_t f = (__float_as_uint(x.scale[FP8 ? i : 0]) >> 16) + (120u << 7), by2 = f | (f << 16);
-                        const uint2 a0 = decode4_fast(x.v[i].x, by2), a1 = decode4_fast(x.v[i].y, by2);
-                        const uint2 b0 = decode4_fast(x.v[i].z, by2), b1 = decode4_fast(x.v[i].w, by2);
-                        put(base + i * (kStep * 128), (line0 + kStep * i) & 7, make_uint4(a0.x, a0.y, a1.x, a1.y),
-                            make_uint4(b0.x, b0.y, b1.x, b1.y));
+                        const uint32_t f = (__float_as_uint(x.scale[i]) >> 16) + (120u << 7), by2 = f | (f << 16);
+                        const uint2 a0 = decode4_fast(x.lo[i].x, by2), a1 = decode4_fast(x.lo[i].y, by2);
+                        const uint2 b0 = decode4_fast(x.hi[i].x, by2), b1 = decode4_fast(x.hi[i].y, by2);
+                        unsigned char *line = base + i * 512 + ((vec ^ ((line0 + 4 * i) & 7)) << 4);
+                        *reinterpret_cast<uint4 *>(line) = make_uint4(a0.x, a0.y, a1.x, a1.y);
+                        *reinterpret_cast<uint4 *>(line + F::half_bytes) = make_uint4(b0.x, b0.y, b1.x, b1.y);
                     }
                 } else {
 #pragma unroll 1
                     for (int i = 0; i < kLoads; ++i) {
-                        uint4 c = x.v[0];
+                        uint2 lo = x.lo[0], hi = x.hi[0];
                         float f = x.scale[0];
 #pragma unroll
                         for (int j = 1; j < kLoads; ++j) {
-                            c = i == j ? x.v[j] : c;
-                            f = i == j ? x.scale[FP8 ? j : 0] : f;
+                            lo = i == j ? x.lo[j] : lo;
+                            hi = i == j ? x.hi[j] : hi;
+                            f = i == j ? x.scale[j] : f;
                         }
-                        const uint2 a0 = decode4_exact(c.x, f), a1 = decode4_exact(c.y, f);
-                        const uint2 b0 = decode4_exact(c.z, f), b1 = decode4_exact(c.w, f);
-                        put(base + i * (kStep * 128), (line0 + kStep * i) & 7, make_uint4(a0.x, a0.y, a1.x, a1.y),
-                            make_uint4(b0.x, b0.y, b1.x, b1.y));
+                        const uint2 a0 = decode4_exact(lo.x, f), a1 = decode4_exact(lo.y, f);
+                        const uint2 b0 = decode4_exact(hi.x, f), b1 = decode4_exact(hi.y, f);
+                        unsigned char *line = base + i * 512 + ((vec ^ ((line0 + 4 * i) & 7)) << 4);
+                        *reinterpret_cast<uint4 *>(line) = make_uint4(a0.x, a0.y, a1.x, a1.y);
+                        *reinterpret_cast<uint4 *>(line + F::half_bytes) = make_uint4(b0.x, b0.y, b1.x, b1.y);
                     }
                 }
+                if (sg + 1 < kGroups) fetch(x);
             }
-            if (++sg < kGroups) return;
-            sg = 0;
             fence_proxy_async_shared();
             __syncwarp();
             if (lane == 0) mbar_arrive(&m->full[stage]);
-            next_stage();
-        };
-        Held x[kAhead];
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) fetch(x[i]);
-        for (int g = 0; g < total; g += kAhead) {
-#pragma unroll
-            for (int i = 0; i < kAhead; ++i) {
-                store(g + i, x[i]);
-                fetch(x[i]);
-            }
+            stage += S;
+            if (stage >= F::ring) stage -= F::ring, phase ^= 1;
+            fetch(x);
         }
+        chunks += total;
     }
 };
 
@@ -690,39 +703,34 @@ struct Softmax {
         int pos0;          // position of line 0
         const int *ends;
     };
-    __device__ __forceinline__ float masked(const Mask &a, float v, int h, int i) const
+    // Scores that a mask leaves out become the infinity whose weight is 0; those of a cache row that is taken
+    // out (`dirty`) and not masked become NaN.
+    __device__ __forceinline__ void mask_all(float x[H][X], const Mask &a, uint32_t dirty) const
     {
-        const int r = (i >> 1) & 1, c = ((i >> 2) << 1) | (i & 1);
-        const bool in = ((a.valid >> (2 * h + r)) & 1u) && !(a.edges && a.pos0 + line(h, r) >= a.ends[col(c)]);
-        return in ? v : -INFINITY;
-    }
-
-    __device__ __forceinline__ void mask_all(float x[H][X], const Mask &mask) const
-    {
+        const float none = k.a.scale_log2 > 0.0f ? -INFINITY : INFINITY;
 #pragma unroll
         for (int h = 0; h < H; ++h)
 #pragma unroll
-            for (int i = 0; i < X; ++i) x[h][i] = masked(mask, x[h][i], h, i);
+            for (int i = 0; i < X; ++i) {
+                const int r = (i >> 1) & 1, c = ((i >> 2) << 1) | (i & 1);
+                const bool in = ((a.valid >> (2 * h + r)) & 1u) && !(a.edges && a.pos0 + line(h, r) >= a.ends[col(c)]);
+                x[h][i] = !in ? none : ((dirty >> (2 * h + r)) & 1u) ? __int_as_float(0x7fffffff) : x[h][i];
+            }
     }
 
-    // Weights outgrow their columns' references (or a column has none yet): new references, sums and
-    // accumulators brought to them, the scores loaded again.
-    __device__ __forceinline__ void move_references(float x[H][X], int buf, bool started, const Mask &mask, bool whole)
+    // Weights outgrow their columns' references, or there are none yet (not `started`): new references, sums
+    // and, where there are `products`, accumulators brought to them.
+    __device__ __forceinline__ void move_references(const float x[H][X], bool started, bool products)
     {
         float2 factor[G];
-        load_scores(x, buf);
-#pragma unroll
-        for (int h = 0; h < H; ++h)
-#pragma unroll
-            for (int i = 0; i < X; ++i) x[h][i] *= k.a.scale_log2;
-        if (!whole) mask_all(x, mask);
 #pragma unroll
         for (int c = 0; c < 2 * G; ++c) {
             float top = -INFINITY;
 #pragma unroll
             for (int h = 0; h < H; ++h)
 #pragma unroll
-                for (int r = 0; r < 2; ++r) top = fmaxf(top, x[h][(c >> 1) * 4 + r * 2 + (c & 1)]);
+                for (int r = 0; r < 2; ++r)
+                    top = fmaxf(top, x[h][(c >> 1) * 4 + r * 2 + (c & 1)] * k.a.scale_log2);
 #pragma unroll
             for (int s = 4; s < 32; s <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
             if (lane < 4) m->part[quad][col(c)] = top;
@@ -731,7 +739,8 @@ struct Softmax {
         auto moved = [&](int c, float &n, float &sum_of) {
             const int at = col(c);
             const float top = fmaxf(fmaxf(m->part[0][at], m->part[1][at]), fmaxf(m->part[2][at], m->part[3][at]));
-            const float now = fmaxf(-n, top + kHeadroom);
+            // (a column without positions so far will have none later: it keeps the reference 0)
+            const float now = top == -INFINITY ? -n : started ? fmaxf(-n, top + kHeadroom) : top + kHeadroom;
             const float f = -n == now ? 1.0f : exp2_approx(-n - now);
             n = -now;
             sum_of *= f;
@@ -742,10 +751,11 @@ struct Softmax {
             factor[g].x = moved(2 * g, neg[g].x, sum[g].x);
             factor[g].y = moved(2 * g + 1, neg[g].y, sum[g].y);
         }
-        if (started) {
+        if (products) {
             wait(&m->pv_done[(tile - 1) & 1], ((tile - 1) >> 1) & 1);
             tmem_fence_after();
             const int vchunks = (k.a.dv + 127) >> 7;
+#pragma unroll 1
             for (int c = 0; c < 2 * vchunks; ++c) {
                 const uint32_t at = o_tm + (c >> 1) * N + (static_cast<uint32_t>((c & 1) * 16) << 16);
                 float o[X];
@@ -757,14 +767,11 @@ struct Softmax {
             }
             tmem_wait_st();
         }
-        load_scores(x, buf);
     }
 
     // A tile's weights 2^(score * scale - reference), two positions by G pairs of columns a block, as bf16
     // pairs; added to `to`.  Returns whether one is 2 or more (or NaN).
-    template <bool WHOLE>
-    __device__ __forceinline__ bool weights_of(const float x[H][X], const Mask &mask, uint32_t dirty,
-                                               uint32_t out[H][2 * G], float2 to[G]) const
+    __device__ __forceinline__ bool weights(const float x[H][X], uint32_t out[H][2 * G], float2 to[G]) const
     {
         const float2 scale = make_float2(k.a.scale_log2, k.a.scale_log2);
         uint32_t any = 0;
@@ -774,29 +781,13 @@ struct Softmax {
             for (int g = 0; g < G; ++g)
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    const int i = 4 * g + 2 * r;
-                    float2 y = fma2(make_float2(x[h][i], x[h][i + 1]), scale, neg[g]);
-                    if (!WHOLE) {
-                        // (a column without positions has no finite reference: its scores are all masked)
-                        y.x = masked(mask, y.x, h, i);
-                        y.y = masked(mask, y.y, h, i + 1);
-                        if ((dirty >> (2 * h + r)) & 1u) {
-                            y.x = y.x != -INFINITY ? __int_as_float(0x7fffffff) : y.x;
-                            y.y = y.y != -INFINITY ? __int_as_float(0x7fffffff) : y.y;
-                        }
-                    }
+                    const float2 y = fma2(make_float2(x[h][4 * g + 2 * r], x[h][4 * g + 2 * r + 1]), scale, neg[g]);
                     const float2 p = make_float2(exp2_approx(y.x), exp2_approx(y.y));
                     to[g] = add2(to[g], p);
                     out[h][2 * g + r] = pack_bf16(p.x, p.y);
                     any |= out[h][2 * g + r];
                 }
         return (any & 0x40004000u) != 0;
-    }
-    __device__ __forceinline__ bool weights(const float x[H][X], const Mask &mask, bool whole, uint32_t dirty,
-                                            uint32_t out[H][2 * G], float2 to[G]) const
-    {
-        // (one branch, not one an element: the exponentials of a thread then overlap)
-        return whole ? weights_of<true>(x, mask, dirty, out, to) : weights_of<false>(x, mask, dirty, out, to);
     }
 
     // A position that one row attends to and another does not has weight 0 in the other, but 0 * NaN is
@@ -810,22 +801,26 @@ struct Softmax {
 #pragma unroll
             for (int r = 0; r < 2; ++r)
                 if (((mask.valid >> (2 * h + r)) & 1u) && !(fabsf(x[h][2 * r]) < INFINITY)) dirty |= 1u << (2 * h + r);
-        if (!bar_any(5, kSoftWarps * 32, dirty != 0)) return 0;
+        if (!bar_any(5, F::soft_warps * 32, dirty != 0)) return 0;
         const int stage0 = static_cast<int>((static_cast<int64_t>(tile) * C) % F::ring);
         auto unit16 = [&](int at, int e) {
             return smem + ((stage0 + (e >> 7)) % F::ring) * F::chunk_bytes + ((e >> 6) & 1) * F::half_bytes + at * 128 +
                    ((((e >> 3) & 7) ^ (at & 7)) << 4);
         };
+#pragma unroll 1
         for (int b = 0; b < 2 * H; ++b) {
             if (!((dirty >> b) & 1u)) continue;
             bool bad = false;
+#pragma unroll 1
             for (int e = 0; e < k.a.dv; ++e)
                 bad |= (reinterpret_cast<const uint16_t *>(unit16(line(b >> 1, b & 1), e))[e & 7] & 0x7f80u) == 0x7f80u;
             if (!bad) dirty &= ~(1u << b);
         }
-        bar_sync(5, kSoftWarps * 32);
+        bar_sync(5, F::soft_warps * 32);
+#pragma unroll 1
         for (int b = 0; b < 2 * H; ++b)
             if (((dirty >> b) & 1u) && group == 0 && (lane & 3) == 0)
+#pragma unroll 1
                 for (int e = 0; e < k.a.dv; e += 8)
                     *reinterpret_cast<uint4 *>(unit16(line(b >> 1, b & 1), e)) = make_uint4(0u, 0u, 0u, 0u);
         return dirty;
@@ -834,7 +829,9 @@ struct Softmax {
     __device__ __forceinline__ void tiles(const Unit &w)
     {
         const int n = w.n;
+        bool started = false;  // a tile with a position has been there
         const uint32_t vshift = line(0, 0) & 31;  // the thread's first position within its word of validity bits
+#pragma unroll 1
         for (int it = 0; it < n; ++it, ++tile) {
             const int buf = tile & 1;
             Mask mask;
@@ -843,26 +840,38 @@ struct Softmax {
             mask.edges = !k.a.idx && mask.pos0 + F::M > w.min_end && w.min_end < w.max_end;
             wait(&m->s_full[buf], (tile >> 1) & 1);
             tmem_fence_after();
-            const uint32_t word = m->valid[tile & (kValidSlots - 1)][line(0, 0) >> 5];
+            const uint4 words = *reinterpret_cast<const uint4 *>(m->valid[tile & (kValidSlots - 1)]);
             float x[H][X];
             load_scores(x, buf);
+            const uint32_t word = quad < 2 ? (quad == 0 ? words.x : words.y) : (quad == 2 ? words.z : words.w);
             mask.valid = 0;
 #pragma unroll
             for (int b = 0; b < 2 * H; ++b) mask.valid |= ((word >> (vshift + 8 * b)) & 1u) << b;
-            const uint32_t dirty = mask.edges ? take_out(x, mask) : 0u;
-            const bool whole = __all_sync(0xffffffffu, mask.valid == (1u << (2 * H)) - 1u) && !mask.edges;
-            // the first tile sets the references, a later one moves them when a weight outgrows its own
-            if (it == 0) move_references(x, buf, false, mask, whole);
+            const bool whole = word == 0xffffffffu && !mask.edges;
+            uint32_t dirty = 0;
+            if (!whole) {
+                if (mask.edges) dirty = take_out(x, mask);
+                mask_all(x, mask, dirty);
+            }
+            // the first tile with a position sets the references, a later one moves them when a weight outgrows
+            // its own
+            bool set = false;
+            if (!started) {
+                set = started = (words.x | words.y | words.z | words.w) != 0;
+                if (started) move_references(x, false, false);
+            }
             uint32_t out[H][2 * G];
             float2 to[G];
 #pragma unroll
             for (int g = 0; g < G; ++g) to[g] = sum[g];
-            const bool over = weights(x, mask, whole, dirty, out, to);
-            if (it > 0 && bar_any(1 + group, 128, over)) {
-                move_references(x, buf, true, mask, whole);
+            const bool over = weights(x, out, to);
+            if (!set && bar_any(1 + group, 128, over)) {
+                load_scores(x, buf);  // (not kept: registers)
+                if (!whole) mask_all(x, mask, dirty);
+                move_references(x, true, it > 0);
 #pragma unroll
                 for (int g = 0; g < G; ++g) to[g] = sum[g];
-                weights(x, mask, whole, dirty, out, to);
+                weights(x, out, to);
             }
 #pragma unroll
             for (int g = 0; g < G; ++g) sum[g] = to[g];
@@ -897,7 +906,7 @@ struct Softmax {
         auto out_row = [&](int c) { return static_cast<int64_t>(w.out[c]); };
 #pragma unroll
         for (int g = 0; g < G; ++g) {
-            neg[g] = make_float2(INFINITY, INFINITY);
+            neg[g] = make_float2(0.0f, 0.0f);
             sum[g] = make_float2(0.0f, 0.0f);
         }
         tiles(w);
@@ -934,6 +943,7 @@ struct Softmax {
         const int vchunks = (k.a.dv + 127) >> 7;
         if (k.p.parts > 1) {
             // (a part without positions has the sum 0: its accumulators are not read)
+#pragma unroll 1
             for (int b = 0; n > 0 && b < 2 * vchunks; ++b) {
                 float o[X];
                 tmem_ld<G>(o_tm + (b >> 1) * N + (static_cast<uint32_t>((b & 1) * 16) << 16), o);
@@ -950,18 +960,19 @@ struct Softmax {
             }
             return;
         }
-        // the group's columns x 128 elements through its quarter of a P buffer pair (free by now), so that
-        // whole 16-byte vectors of a column are written; unit u of column j lies at unit u ^ (j mod 16)
-        unsigned char *stage = smem + F::p_off + group * (W * 256);
-        float inv[2 * G];
+        // A warp's columns x 32 elements through its part of a P buffer (free by now), so that whole 16-byte
+        // vectors of a column are written; unit u of column j lies at unit u ^ (j / 2 mod 4).
+        unsigned char *stage = smem + F::p_off + (group * 4 + quad) * (W * 64);
+        float2 inv[G];
 #pragma unroll
-        for (int c = 0; c < 2 * G; ++c) inv[c] = m->inv[col(c)];
-        uint16_t *to[W / 8];  // the vectors this thread writes: column, element 8 (lane mod 16); null: unused
+        for (int g = 0; g < G; ++g) inv[g] = make_float2(m->inv[col(2 * g)], m->inv[col(2 * g + 1)]);
+        uint16_t *to[W / 8];  // the vectors this thread writes; null: unused
 #pragma unroll
         for (int i = 0; i < W / 8; ++i) {
-            const int at = group * W + quad * (W / 4) + i * 2 + (lane >> 4);
-            to[i] = at < cols ? k.a.out + out_row(at) * k.a.dv + (lane & 15) * 8 : nullptr;
+            const int at = group * W + i * 8 + (lane >> 2);
+            to[i] = at < cols ? k.a.out + out_row(at) * k.a.dv + quad * 32 + (lane & 3) * 8 : nullptr;
         }
+#pragma unroll 1
         for (int ch = 0; ch < vchunks; ++ch) {
             float o[2][X];
             if (n > 0) {
@@ -980,22 +991,22 @@ struct Softmax {
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {  // as P^T's blocks, stored transposed: 8 elements of a column a line
                         const int gg = g + (q >> 1), i = 4 * gg + 2 * (q & 1);
-                        out[q] = pack_bf16(o[b][i] * inv[2 * gg], o[b][i + 1] * inv[2 * gg + 1]);
+                        out[q] = pack_bf16(o[b][i] * inv[gg].x, o[b][i + 1] * inv[gg].y);
                     }
-                    const int j = (g + (lane >> 4)) * 8 + (lane & 7), u = quad * 4 + b * 2 + ((lane >> 3) & 1);
-                    stmatrix4_trans(smem_addr(stage) + j * 256 + ((u ^ (j & 15)) << 4), out);
+                    const int j = (g + (lane >> 4)) * 8 + (lane & 7), u = b * 2 + ((lane >> 3) & 1);
+                    stmatrix4_trans(smem_addr(stage) + j * 64 + ((u ^ ((j >> 1) & 3)) << 4), out);
                 }
-            bar_sync(bar, 128);
+            __syncwarp();
 #pragma unroll
             for (int i = 0; i < W / 8; ++i) {
-                const int j = quad * (W / 4) + i * 2 + (lane >> 4), u = lane & 15;
-                if (to[i] && ch * 128 + u * 8 < k.a.dv)
+                const int j = i * 8 + (lane >> 2), u = lane & 3;
+                if (to[i] && ch * 128 + quad * 32 + u * 8 < k.a.dv)
                     __stcs(reinterpret_cast<uint4 *>(to[i] + ch * 128),
-                           *reinterpret_cast<const uint4 *>(stage + j * 256 + ((u ^ (j & 15)) << 4)));
+                           *reinterpret_cast<const uint4 *>(stage + j * 64 + ((u ^ ((j >> 1) & 3)) << 4)));
             }
-            bar_sync(bar, 128);
+            __syncwarp();
         }
-        bar_sync(5, kSoftWarps * 32);  // the next unit's P covers every group's staging
+        bar_sync(5, F::soft_warps * 32);  // the next unit's P covers every warp's staging
     }
 };
 
@@ -1010,25 +1021,25 @@ __global__ void __launch_bounds__(Cfg<C, N, FP8>::threads, 1) attention_kernel(c
     const int64_t units = k.p.items * k.p.parts;
     if (t == 0) {
         for (int i = 0; i < F::ring; ++i) {
-            mbar_init(&m->full[i], FP8 ? F::load_warps : F::load_warps * 32);
+            mbar_init(&m->full[i], FP8 ? F::set_warps : F::load_warps * 32);
             mbar_init(&m->empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&m->s_full[i], 1);
-            mbar_init(&m->s_empty[i], kSoftWarps);
-            mbar_init(&m->p_full[i], kSoftWarps);
+            mbar_init(&m->s_empty[i], F::soft_warps);
+            mbar_init(&m->p_full[i], F::soft_warps);
             mbar_init(&m->pv_done[i], 1);
         }
         for (int i = 0; i < kUnits; ++i) {
             mbar_init(&m->unit_full[i], 1);
-            mbar_init(&m->unit_empty[i], kSoftWarps + 3 + F::load_warps);
+            mbar_init(&m->unit_empty[i], F::soft_warps + 3 + F::load_warps);
         }
         mbar_init(&m->q_full, 2);
         mbar_init(&m->q_empty, 1);
         fence_mbar_init();
         m->abort = 0;
     }
-    if (warp == kMmaWarp) tmem_alloc(&m->tmem, 512);
+    if (warp == F::mma_warp) tmem_alloc(&m->tmem, 512);
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
@@ -1043,19 +1054,20 @@ __global__ void __launch_bounds__(Cfg<C, N, FP8>::threads, 1) attention_kernel(c
         if (lane == 0) mbar_arrive(&m->unit_empty[i % kUnits]);
     };
 
-    if (warp < kSoftWarps) {
+    if (warp < F::soft_warps) {
         regs_to<F::soft_regs, (F::soft_regs > F::launch_regs)>();
         const int group = warp >> 2, quad = warp & 3;
         const uint32_t at = m->tmem + (static_cast<uint32_t>(quad * 32) << 16) + group * F::cols_per_group;
         Softmax<C, N, FP8> soft{k, m, wait, smem, group, quad, lane, at, at + C * N};
         int i = 0;
+#pragma unroll 1
         for (int64_t u = blockIdx.x; u < units; u += gridDim.x, ++i) {
             soft.unit(*take(i));
             give(i);
         }
-    } else if (warp < kLoadWarp0) {
+    } else if (warp < F::load_warp0) {
         regs_to<F::mma_regs, false>();
-        if (warp == kMmaWarp) {
+        if (warp == F::mma_warp) {
             Issuer<C, N, FP8> issue{m, wait};
             issue.ring_k = umma_desc(smem_addr(smem), 16, 1024);
             issue.ring_v = umma_desc(smem_addr(smem), F::half_bytes, 1024);
@@ -1067,13 +1079,15 @@ __global__ void __launch_bounds__(Cfg<C, N, FP8>::threads, 1) attention_kernel(c
             issue.halves = (k.a.d + 63) >> 6;
             issue.vchunks = (k.a.dv + 127) >> 7;
             int i = 0, loaded = 0;
+#pragma unroll 1
             for (int64_t u = blockIdx.x; u < units; u += gridDim.x, ++i) {
                 const int n = __reduce_max_sync(0xffffffffu, take(i)->n);
                 if (n > 0) issue.unit(n, loaded++ & 1);
                 give(i);
             }
-        } else if (warp == kUnitWarp) {
+        } else if (warp == F::unit_warp) {
             int i = 0;
+#pragma unroll 1
             for (int64_t u = blockIdx.x; u < units; u += gridDim.x, ++i) {
                 wait(&m->unit_empty[i % kUnits], ((i / kUnits) & 1) ^ 1);
                 make_unit<N, F::M>(k, u, &m->unit[i % kUnits], lane);
@@ -1082,26 +1096,31 @@ __global__ void __launch_bounds__(Cfg<C, N, FP8>::threads, 1) attention_kernel(c
             }
         } else {
             int i = 0, loaded = 0;
+#pragma unroll 1
             for (int64_t u = blockIdx.x; u < units; u += gridDim.x, ++i) {
                 const Unit *w = take(i);
                 if (w->n > 0) {
                     wait(&m->q_empty, (loaded++ & 1) ^ 1);
-                    load_queries<C, N, FP8>(k, w, m, smem, warp - kUnitWarp - 1, lane);
+                    load_queries<C, N, FP8>(k, w, m, smem, warp - F::unit_warp - 1, lane);
                 }
                 give(i);
             }
         }
     } else {
         regs_to<F::load_regs, (F::load_regs > F::launch_regs)>();
-        Loader<C, N, FP8> load{k, m, wait, smem, lane, warp - kLoadWarp0};
+        const int set = (warp - F::load_warp0) / F::set_warps;
+        Loader<C, N, FP8> load{k, m, wait, smem, lane, (warp - F::load_warp0) % F::set_warps};
+        load.stage = set;  // (sets take the stages in turn)
         int i = 0;
+#pragma unroll 1
         for (int64_t u = blockIdx.x; u < units; u += gridDim.x, ++i) {
             load.w = take(i);
             if (load.w->n > 0) {
                 if (FP8)
-                    load.rows_held();
+                    load.rows_codes(set);
                 else
                     load.rows_bf16();
+                load.tile += load.w->n;
             }
             give(i);
         }
@@ -1109,7 +1128,7 @@ __global__ void __launch_bounds__(Cfg<C, N, FP8>::threads, 1) attention_kernel(c
     }
     tmem_fence_before();
     __syncthreads();
-    if (warp == kMmaWarp) tmem_dealloc(m->tmem, 512);
+    if (warp == F::mma_warp) tmem_dealloc(m->tmem, 512);
 }
 
 // Joins the parts of each (row, head): out = sum_p 2^(ref_p - max) o_p / sum_p 2^(ref_p - max) sum_p.
@@ -1163,7 +1182,7 @@ cudaError_t launch(const Kargs &k, cudaStream_t s)
     constexpr size_t smem = F::misc_off + sizeof(Misc);
     static_assert(smem <= 232448, "more than a CTA may use");
     static_assert(smem > 116 * 1024, "one CTA an SM: each takes all of the tensor memory");
-    static_assert(4 * F::cols_per_group * 256 <= F::pbufs * F::p_bytes, "outputs are staged where P was");
+    static_assert(N * 256 <= F::pbufs * F::p_bytes, "outputs are staged where P was");
     // the attribute is set once on each device (a device past the mask's 64: on each call)
     static std::atomic<uint64_t> set{0};
     int dev = 0;
