@@ -62,10 +62,17 @@ struct Cfg {
     static constexpr int q_half = N * 128;                          // bytes of one
     static constexpr int p_block = M * 128;                         // 64 columns of P^T, a line a position
     static constexpr int p_bytes = N / 64 * p_block;
-    static constexpr int ring = wide && C == 1 ? 3 : (C == 1 ? 5 : 4);  // chunks staged
+    // Chunks staged.  Of rows of 129 to 192 elements the first chunk has 3 places and the second, which is half
+    // as large and often no part of the value, 2 of its own (`own`): three tiles are under way at a time where
+    // a common ring has two.
+    static constexpr bool own = wide && C == 2 && !FP8;
+    static constexpr int ring = own ? 5 : wide && C == 1 ? 3 : (C == 1 ? 5 : 4);
+    static constexpr int ring_bytes = own ? 4 * chunk_bytes : ring * chunk_bytes;
+    static constexpr int own0 = 3;  // places of the first chunk
+    static __device__ __forceinline__ int place(int stage) { return stage * chunk_bytes - (own && stage > own0 ? half_bytes : 0); }
     static constexpr int pbufs = C == 1 || (C == 2 && !wide) ? 2 : 1;
     static constexpr bool ahead = ring >= 2 * C;  // the next tile's scores before this one's values
-    static constexpr int q_off = ring * chunk_bytes;
+    static constexpr int q_off = ring_bytes;
     static constexpr int p_off = q_off + q_halves * q_half;
     static constexpr int misc_off = p_off + pbufs * p_bytes;
     // Warps: groups of 4 for the softmax, an equal share of the columns each; a group of 4 with the one that
@@ -108,7 +115,7 @@ struct Misc {
     uint64_t unit_full[kUnits], unit_empty[kUnits];
     uint32_t tmem;
     int abort;
-    alignas(16) float inv[kMaxCols];      // 1 / sum
+    alignas(16) float inv[kMaxCols];      // references, then 1 / sum
     alignas(16) float part[4][kMaxCols];  // maxima, then sums, of the four warps of a group
     alignas(16) uint32_t valid[kValidSlots][4];  // bit k of word w: position 32 w + k of the tile has a cache row
     alignas(16) Unit unit[kUnits];
@@ -326,6 +333,22 @@ __device__ __forceinline__ uint2 decode4_exact(uint32_t codes, float scale)
     return make_uint2(out[0], out[1]);
 }
 
+// A walk over the places of the ring, chunk by chunk.
+template <typename F>
+struct Walk {
+    int s0 = 0, p0 = 0, s1 = F::own0, p1 = 0;  // stage and phase; of the second chunk, where it has its own
+    __device__ __forceinline__ int stage(int c) const { return F::own && c ? s1 : s0; }
+    __device__ __forceinline__ int phase(int c) const { return F::own && c ? p1 : p0; }
+    __device__ __forceinline__ void next(int c)
+    {
+        if (F::own && c) {
+            if (++s1 == F::ring) s1 = F::own0, p1 ^= 1;
+        } else {
+            if (++s0 == (F::own ? F::own0 : F::ring)) s0 = 0, p0 ^= 1;
+        }
+    }
+};
+
 template <int C, int N, bool FP8>
 struct Loader {
     using F = Cfg<C, N, FP8>;
@@ -340,7 +363,8 @@ struct Loader {
     unsigned char *smem;
     int lane, lw;
     const Unit *w = nullptr;
-    int stage = 0, phase = 1;  // of the ring; a fresh barrier's phase of parity 1 counts as completed
+    Walk<F> at_ring;           // (bf16 rows)
+    int stage = 0, phase = 1;  // (8-bit rows) a fresh barrier's phase of parity 1 counts as completed
     int tile = 0;              // tiles staged in units before
 
     struct Rows {
@@ -394,11 +418,6 @@ struct Loader {
         }
     }
 
-    __device__ __forceinline__ void next_stage()
-    {
-        if (++stage == F::ring) stage = 0, phase ^= 1;
-    }
-
     // ---- bf16 rows: asynchronous copies, whose completion arrives at the chunk's barrier by itself.  (Waiting
     // for them here instead keeps the warp from filling a chunk that has come free meanwhile.)
     __device__ __forceinline__ void rows_bf16()
@@ -424,8 +443,9 @@ struct Loader {
             }
 #pragma unroll 1
             for (int c = 0; c < C; ++c) {
-                wait(&m->empty[stage], phase);
-                const uint32_t base = to + stage * F::chunk_bytes;
+                const int stage = at_ring.stage(c);
+                wait(&m->empty[stage], at_ring.phase(c) ^ 1);
+                const uint32_t base = to + F::place(stage);
                 const int e = c * 128 + vec * 8;
                 const bool used = c * 2 + (vec >> 3) < halves;
 #pragma unroll
@@ -437,7 +457,7 @@ struct Loader {
                                    ok ? 16u : 0u);
                 }
                 cp_async_arrive(&m->full[stage]);
-                next_stage();
+                at_ring.next(c);
             }
         }
     }
@@ -595,7 +615,7 @@ struct Issuer {
     uint64_t ring_k, ring_v, q0, p0;
     uint32_t o_col, s_col;
     int halves, vchunks;  // blocks of 64 elements of a row, of 128 of a value
-    int s_stage = 0, s_phase = 0, v_stage = 0;
+    Walk<F> s_ring, v_ring;
     int s_tile = 0, v_tile = 0;  // tiles issued so far
 
     // A tile's scores.
@@ -607,10 +627,11 @@ struct Issuer {
         wait(&m->s_empty[buf], ((s_tile >> 1) & 1) ^ 1);
 #pragma unroll 1
         for (int c = 0; c < C; ++c) {
-            wait(&m->full[s_stage], s_phase);
+            const int stage = s_ring.stage(c);
+            wait(&m->full[stage], s_ring.phase(c));
             if (!FP8) fence_proxy_async_shared();  // (asynchronous copies arrive without a fence of their own)
             tmem_fence_after();
-            const uint64_t a = ring_k + static_cast<uint32_t>(s_stage * (F::chunk_bytes / 16));
+            const uint64_t a = ring_k + static_cast<uint32_t>(F::place(stage) / 16);
             const uint64_t b = q0 + static_cast<uint32_t>(c * (2 * F::q_half / 16));
             if (elect_one()) {
                 umma_bf16(d, a, b, kScores, c > 0);
@@ -621,9 +642,10 @@ struct Issuer {
                     for (int s = 0; s < 4; ++s)
                         umma_bf16(d, a + F::half_bytes / 16 + s * 2, b + F::q_half / 16 + s * 2, kScores, true);
                 }
+                if (c >= vchunks) umma_commit(&m->empty[stage]);  // (no part of the value: free by then)
             }
             __syncwarp();
-            if (++s_stage == F::ring) s_stage = 0, s_phase ^= 1;
+            s_ring.next(c);
         }
         if (elect_one()) umma_commit(&m->s_full[buf]);
         ++s_tile;
@@ -638,19 +660,20 @@ struct Issuer {
         const uint64_t b = p0 + static_cast<uint32_t>((v_tile % F::pbufs) * (F::p_bytes / 16));
 #pragma unroll 1
         for (int c = 0; c < C; ++c) {
-            const uint64_t a = ring_v + static_cast<uint32_t>(v_stage * (F::chunk_bytes / 16));
+            const int stage = v_ring.stage(c);
+            const uint64_t a = ring_v + static_cast<uint32_t>(F::place(stage) / 16);
             const uint32_t d = o_col + c * N;
             if (elect_one()) {
                 if (c < vchunks) {
                     umma_bf16(d, a, b, kValues, !first);
 #pragma unroll
                     for (int s = 1; s < F::M / 16; ++s) umma_bf16(d, a + s * 128, b + s * 128, kValues, true);
+                    umma_commit(&m->empty[stage]);
                 }
-                umma_commit(&m->empty[v_stage]);
                 if (c + 1 == C) umma_commit(&m->pv_done[buf]);
             }
             __syncwarp();
-            if (++v_stage == F::ring) v_stage = 0;
+            v_ring.next(c);
         }
         ++v_tile;
     }
@@ -708,48 +731,102 @@ struct Softmax {
     __device__ __forceinline__ void mask_all(float x[H][X], const Mask &a, uint32_t dirty) const
     {
         const float none = k.a.scale_log2 > 0.0f ? -INFINITY : INFINITY;
+        if (dirty) {
+#pragma unroll
+            for (int h = 0; h < H; ++h)
+#pragma unroll
+                for (int i = 0; i < X; ++i)
+                    if ((dirty >> (2 * h + ((i >> 1) & 1))) & 1u) x[h][i] = __int_as_float(0x7fffffff);
+        }
+        // a position against the ends: its offset from the thread's first, or past every end without a row
+        int at[H][2];
 #pragma unroll
         for (int h = 0; h < H; ++h)
 #pragma unroll
-            for (int i = 0; i < X; ++i) {
-                const int r = (i >> 1) & 1, c = ((i >> 2) << 1) | (i & 1);
-                const bool in = ((a.valid >> (2 * h + r)) & 1u) && !(a.edges && a.pos0 + line(h, r) >= a.ends[col(c)]);
-                x[h][i] = !in ? none : ((dirty >> (2 * h + r)) & 1u) ? __int_as_float(0x7fffffff) : x[h][i];
+            for (int r = 0; r < 2; ++r) at[h][r] = (a.valid >> (2 * h + r)) & 1u ? h * 16 + r * 8 : 0x7fffffff;
+        const int first = a.pos0 + line(0, 0);
+#pragma unroll
+        for (int c = 0; c < 2 * G; ++c) {
+            const int end = a.edges ? a.ends[col(c)] - first : 0x7fffffff;
+#pragma unroll
+            for (int h = 0; h < H; ++h)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    float &v = x[h][(c >> 1) * 4 + r * 2 + (c & 1)];
+                    v = at[h][r] >= end ? none : v;
+                }
+        }
+    }
+
+    // The thread's 2 G columns reduced over the 8 lanes that share them: the lane is left with one column, its
+    // column own().  (Fewer instructions than a butterfly a column; what runs once a unit waits for them.)
+    __device__ __forceinline__ int own() const
+    {
+        return G == 4 ? ((lane >> 4) & 1) * 4 + ((lane >> 3) & 1) * 2 + ((lane >> 2) & 1)
+                      : ((lane >> 4) & 1) * 2 + ((lane >> 3) & 1);
+    }
+    template <typename Op>
+    __device__ __forceinline__ float over_lanes(float v[2 * G], Op op) const
+    {
+        static_assert(G == 2 || G == 4, "");
+        int n = 2 * G;
+#pragma unroll
+        for (int s = 16; s >= 4; s >>= 1) {
+            if (n > 1) {
+                n /= 2;
+                const bool up = (lane & s) != 0;
+#pragma unroll
+                for (int i = 0; i < G; ++i)
+                    if (i < n) v[i] = op(up ? v[i + n] : v[i], __shfl_xor_sync(0xffffffffu, up ? v[i] : v[i + n], s));
+            } else {
+                v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], s));
             }
+        }
+        return v[0];
+    }
+    // Of the thread's columns: its own one's value, and each column's from the lane that owns it.
+    __device__ __forceinline__ float pick(const float2 v[G]) const
+    {
+        const int c = own();
+        float out = v[0].x;
+#pragma unroll
+        for (int i = 1; i < 2 * G; ++i) out = c == i ? ((i & 1) ? v[i >> 1].y : v[i >> 1].x) : out;
+        return out;
+    }
+    __device__ __forceinline__ float from_own(float v, int c) const
+    {
+        return __shfl_sync(0xffffffffu, v, (c << (G == 4 ? 2 : 3)) | (lane & 3));
     }
 
     // Weights outgrow their columns' references, or there are none yet (not `started`): new references, sums
     // and, where there are `products`, accumulators brought to them.
     __device__ __forceinline__ void move_references(const float x[H][X], bool started, bool products)
     {
-        float2 factor[G];
+        float top[2 * G];
 #pragma unroll
         for (int c = 0; c < 2 * G; ++c) {
-            float top = -INFINITY;
+            top[c] = -INFINITY;
 #pragma unroll
             for (int h = 0; h < H; ++h)
 #pragma unroll
                 for (int r = 0; r < 2; ++r)
-                    top = fmaxf(top, x[h][(c >> 1) * 4 + r * 2 + (c & 1)] * k.a.scale_log2);
-#pragma unroll
-            for (int s = 4; s < 32; s <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
-            if (lane < 4) m->part[quad][col(c)] = top;
+                    top[c] = fmaxf(top[c], x[h][(c >> 1) * 4 + r * 2 + (c & 1)] * k.a.scale_log2);
         }
+        const int at = col(own());
+        m->part[quad][at] = over_lanes(top, [](float a, float b) { return fmaxf(a, b); });
         bar_sync(1 + group, 128);
-        auto moved = [&](int c, float &n, float &sum_of) {
-            const int at = col(c);
-            const float top = fmaxf(fmaxf(m->part[0][at], m->part[1][at]), fmaxf(m->part[2][at], m->part[3][at]));
-            // (a column without positions so far will have none later: it keeps the reference 0)
-            const float now = top == -INFINITY ? -n : started ? fmaxf(-n, top + kHeadroom) : top + kHeadroom;
-            const float f = -n == now ? 1.0f : exp2_approx(-n - now);
-            n = -now;
-            sum_of *= f;
-            return f;
-        };
+        const float most = fmaxf(fmaxf(m->part[0][at], m->part[1][at]), fmaxf(m->part[2][at], m->part[3][at]));
+        const float was = -pick(neg);
+        // (a column without positions so far will have none later: it keeps the reference 0)
+        const float now = most == -INFINITY ? was : started ? fmaxf(was, most + kHeadroom) : most + kHeadroom;
+#pragma unroll
+        for (int g = 0; g < G; ++g) neg[g] = make_float2(-from_own(now, 2 * g), -from_own(now, 2 * g + 1));
+        if (!started) return;  // (nothing to rescale)
+        const float by = was == now ? 1.0f : exp2_approx(was - now);
 #pragma unroll
         for (int g = 0; g < G; ++g) {
-            factor[g].x = moved(2 * g, neg[g].x, sum[g].x);
-            factor[g].y = moved(2 * g + 1, neg[g].y, sum[g].y);
+            sum[g].x *= from_own(by, 2 * g);
+            sum[g].y *= from_own(by, 2 * g + 1);
         }
         if (products) {
             wait(&m->pv_done[(tile - 1) & 1], ((tile - 1) >> 1) & 1);
@@ -762,7 +839,7 @@ struct Softmax {
                 tmem_ld<G>(at, o);
                 tmem_wait_ld();
 #pragma unroll
-                for (int i = 0; i < X; ++i) o[i] *= (i & 1) ? factor[i >> 2].y : factor[i >> 2].x;
+                for (int i = 0; i < X; ++i) o[i] *= from_own(by, 2 * (i >> 2) + (i & 1));
                 tmem_st<G>(at, o);
             }
             tmem_wait_st();
@@ -804,7 +881,9 @@ struct Softmax {
         if (!bar_any(5, F::soft_warps * 32, dirty != 0)) return 0;
         const int stage0 = static_cast<int>((static_cast<int64_t>(tile) * C) % F::ring);
         auto unit16 = [&](int at, int e) {
-            return smem + ((stage0 + (e >> 7)) % F::ring) * F::chunk_bytes + ((e >> 6) & 1) * F::half_bytes + at * 128 +
+            const int c = e >> 7;
+            const int stage = !F::own ? (stage0 + c) % F::ring : c ? F::own0 + tile % (F::ring - F::own0) : tile % F::own0;
+            return smem + F::place(stage) + ((e >> 6) & 1) * F::half_bytes + at * 128 +
                    ((((e >> 3) & 7) ^ (at & 7)) << 4);
         };
 #pragma unroll 1
@@ -912,27 +991,25 @@ struct Softmax {
         tiles(w);
         // column sums, in a fixed order
         bar_sync(bar, 128);
+        {
+            float l[2 * G];
 #pragma unroll
-        for (int c = 0; c < 2 * G; ++c) {
-            float l = (c & 1) ? sum[c >> 1].y : sum[c >> 1].x;
-#pragma unroll
-            for (int s = 4; s < 32; s <<= 1) l += __shfl_xor_sync(0xffffffffu, l, s);
-            if (lane < 4) m->part[quad][col(c)] = l;
+            for (int c = 0; c < 2 * G; ++c) l[c] = (c & 1) ? sum[c >> 1].y : sum[c >> 1].x;
+            const int at = col(own());
+            m->part[quad][at] = over_lanes(l, [](float a, float b) { return a + b; });
+            if (quad == 0) m->inv[at] = -pick(neg);
         }
         bar_sync(bar, 128);
-        if (quad == 0 && lane < 4) {
-#pragma unroll
-            for (int c = 0; c < 2 * G; ++c) {
-                const int at = col(c);
-                const float l = (m->part[0][at] + m->part[1][at]) + (m->part[2][at] + m->part[3][at]);
-                const float ref = (c & 1) ? -neg[c >> 1].y : -neg[c >> 1].x;
-                m->inv[at] = l == 0.0f ? 0.0f : 1.0f / l;
-                if (at < cols) {
-                    if (k.p.parts > 1)
-                        k.part_ml[out_row(at) * k.p.parts + w.part] = make_float2(ref, l);
-                    else if (k.a.lse)
-                        k.a.lse[out_row(at)] = l == 0.0f ? -INFINITY : (ref + log2f(l)) * 0.69314718055994531f;
-                }
+        if (quad == 0 && lane < W) {  // a column a lane
+            const int at = group * W + lane;
+            const float l = (m->part[0][at] + m->part[1][at]) + (m->part[2][at] + m->part[3][at]);
+            const float ref = m->inv[at];
+            m->inv[at] = l == 0.0f ? 0.0f : 1.0f / l;
+            if (at < cols) {
+                if (k.p.parts > 1)
+                    k.part_ml[out_row(at) * k.p.parts + w.part] = make_float2(ref, l);
+                else if (k.a.lse)
+                    k.a.lse[out_row(at)] = l == 0.0f ? -INFINITY : (ref + log2f(l)) * 0.69314718055994531f;
             }
         }
         bar_sync(bar, 128);
