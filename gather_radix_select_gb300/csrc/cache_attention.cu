@@ -272,13 +272,13 @@ __device__ __forceinline__ void make_unit(const Kargs &k, int64_t u, Unit *w, in
 
 // ------------------------------------------------------------------------------------ staging rows
 // Loads under a predicate, without a branch; 0 (or `other`) where it is false.
-__device__ __forceinline__ uint2 load8_if(const void *p, bool yes)
+__device__ __forceinline__ uint4 load16_if(const void *p, bool yes)
 {
-    uint2 v;
+    uint4 v;
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %3, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\t"
-        "@p ld.global.nc.v2.u32 {%0, %1}, [%2];\n\t}"
-        : "=&r"(v.x), "=&r"(v.y)
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\t"
+        "mov.b32 %3, 0;\n\t@p ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+        : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
         : "l"(p), "r"(yes ? 1 : 0));
     return v;
 }
@@ -295,11 +295,11 @@ __device__ __forceinline__ float load4_if(const float *p, bool yes, float other)
 // (decodes_fast), a code's exponent and mantissa bits, put where bf16 has them, are its value times 2^-120
 // (subnormal codes give subnormal numbers), and one bf16 product makes that value * scale, rounding only
 // where the result is subnormal.  Else by way of fp32.
-__device__ __forceinline__ bool decodes_fast(uint2 lo, uint2 hi, float scale)
+__device__ __forceinline__ bool decodes_fast(uint4 codes, float scale)
 {
     const uint32_t s = __float_as_uint(scale);
-    const uint32_t nan = ((lo.x & 0x7f7f7f7fu) + 0x01010101u) | ((lo.y & 0x7f7f7f7fu) + 0x01010101u) |
-                         ((hi.x & 0x7f7f7f7fu) + 0x01010101u) | ((hi.y & 0x7f7f7f7fu) + 0x01010101u);
+    const uint32_t nan = ((codes.x & 0x7f7f7f7fu) + 0x01010101u) | ((codes.y & 0x7f7f7f7fu) + 0x01010101u) |
+                         ((codes.z & 0x7f7f7f7fu) + 0x01010101u) | ((codes.w & 0x7f7f7f7fu) + 0x01010101u);
     return ((s & 0x007fffffu) | (nan & 0x80808080u)) == 0 && s - 0x00800000u < (134u << 23);
 }
 
@@ -464,15 +464,13 @@ struct Loader {
 
     // ---- 8-bit rows: loaded to registers a group ahead, decoded to bf16 on the way to shared memory.  (Two
     // groups ahead were measured slower, 188 against 157 us for 1024 rows over 512 selected positions of 512;
-    // a second set of warps, with chunks of its own, hides the loads instead.)  A lane takes codes 8 v .. and
-    // 64 + 8 v .. of a line's 128 (v = lane mod 8): the 8 lanes of a line then store its 8 units of either half,
-    // without bank conflicts.
+    // a second set of warps, with chunks of its own, hides the loads instead.)  A lane takes codes 16 v .. of a
+    // line's 128 (v = lane mod 8), two units of 16 bytes of bf16; lanes 4 .. 7 of a line, whose units are in its
+    // other half, store the second first: without bank conflicts.  A tile's scales are loaded by a line a lane,
+    // and passed on.
     static constexpr int kLoads = kVecs < 4 ? kVecs : 4;           // lines of a group
     static constexpr int kGroups = (kVecs + kLoads - 1) / kLoads;  // groups of a chunk
-    struct Codes {
-        uint2 lo[kLoads], hi[kLoads];
-        float scale[kLoads];
-    };
+    static constexpr int kScales = kPos == 32 ? C : 1;  // scales of a lane: its line's, or one of its line's chunks
     int chunks = 0;  // staged in units before, by all sets
 
     __device__ __forceinline__ void rows_codes(int set)
@@ -487,32 +485,31 @@ struct Loader {
         bool fresh = true;                              // rows of tile ft not looked up yet
         int64_t pos = position(ft + kNext);
         Place at = page_of(position(ft));
-        const uint8_t *from[kVecs];  // null: no row
-        const float *by[kVecs];
-        auto fetch = [&](Codes &x) {
+        int64_t mine = -1;  // row of the lane's line; -1: none
+        float sc[kScales];
+        uint4 x[kLoads];
+        auto fetch = [&]() {
             if (ft >= w->n) return;
             if (fresh) {
                 const Rows cur = row_of(at);
                 if (fc == 0) note(ft, cur);
                 at = page_of(pos);
                 pos = position(ft + 2 * kNext);
+                if (kPos == 32) {
 #pragma unroll
-                for (int i = 0; i < kVecs; ++i) {
-                    const int64_t row = __shfl_sync(0xffffffffu, cur.row, 4 * i + (lane >> 3));
-                    from[i] = row < 0 ? nullptr : data + row + vec * 8;
-                    by[i] = scales + __shfl_sync(0xffffffffu, cur.scale, 4 * i + (lane >> 3));
+                    for (int i = 0; i < kScales; ++i) sc[i] = load4_if(scales + cur.scale + i, cur.row >= 0 && i * 128 < d, 1.0f);
+                } else {  // (with 16 lines a warp, its chunks of the tile are fc and fc + 2)
+                    const int c = fc + 2 * (lane >> 4);
+                    sc[0] = load4_if(scales + cur.scale + c, cur.row >= 0 && c * 128 < d, 1.0f);
                 }
+                mine = cur.row;
                 fresh = false;
             }
-            const bool in = fc * 128 + vec * 8 < d, in_hi = fc * 128 + 64 + vec * 8 < d;
+            const bool in = fc * 128 + vec * 16 < d;
 #pragma unroll
             for (int i = 0; i < kLoads; ++i) {
-                const int late = kVecs - kLoads + i;
-                const uint8_t *f = kGroups == 1 || fg == 0 ? from[i] : from[late];
-                const float *s = kGroups == 1 || fg == 0 ? by[i] : by[late];
-                x.lo[i] = load8_if(f + fc * 128, f && in);
-                x.hi[i] = load8_if(f + fc * 128 + 64, f && in_hi);
-                x.scale[i] = load4_if(s + fc, f && in, 1.0f);
+                const int64_t row = __shfl_sync(0xffffffffu, mine, (fg * kLoads + i) * 4 + (lane >> 3));
+                x[i] = load16_if(data + row + fc * 128 + vec * 16, row >= 0 && in);
             }
             if (++fg < kGroups) return;
             fg = 0;
@@ -524,55 +521,60 @@ struct Loader {
             }
         };
         static_assert(!FP8 || kGroups <= 2, "");
-        const int line0 = lw * kPos + (lane >> 3);
-        unsigned char *to = smem + line0 * 128;
-        Codes x;
-        fetch(x);
+        const int line0 = lw * kPos + (lane >> 3), swap = vec >> 2;
+        unsigned char *to = smem + (vec >> 2) * F::half_bytes + line0 * 128;
+        int c = g % C;  // chunk of the tile
+        fetch();
 #pragma unroll 1
         for (; g < total; g += S) {
             wait(&m->empty[stage], phase);
 #pragma unroll 1
             for (int sg = 0; sg < kGroups; ++sg) {
                 unsigned char *base = to + stage * F::chunk_bytes + sg * (kLoads * 4 * 128);
+                float scale[kLoads];
                 bool fast = true;
 #pragma unroll
-                for (int i = 0; i < kLoads; ++i) fast &= decodes_fast(x.lo[i], x.hi[i], x.scale[i]);
+                for (int i = 0; i < kLoads; ++i) {
+                    const int line = (sg * kLoads + i) * 4 + (lane >> 3);
+                    scale[i] = kPos == 32 ? __shfl_sync(0xffffffffu, c == 0 ? sc[0] : sc[kScales - 1], line)
+                                          : __shfl_sync(0xffffffffu, sc[0], line + 16 * (c >> 1));
+                    fast &= decodes_fast(x[i], scale[i]);
+                }
+                auto store = [&](int i, uint2 a0, uint2 a1, uint2 b0, uint2 b1) {
+                    unsigned char *line = base + i * 512;
+                    const int at7 = (line0 + 4 * i) & 7, u = (2 * vec & 7) + swap;
+                    *reinterpret_cast<uint4 *>(line + ((u ^ at7) << 4)) = make_uint4(a0.x, a0.y, a1.x, a1.y);
+                    *reinterpret_cast<uint4 *>(line + (((u ^ 1) ^ at7) << 4)) = make_uint4(b0.x, b0.y, b1.x, b1.y);
+                };
                 if (fast) {
 #pragma unroll
                     for (int i = 0; i < kLoads; ++i) {
-                        const uint32_t f = (__float_as_uint(x.scale[i]) >> 16) + (120u << 7), by2 = f | (f << 16);
-                        const uint2 a0 = decode4_fast(x.lo[i].x, by2), a1 = decode4_fast(x.lo[i].y, by2);
-                        const uint2 b0 = decode4_fast(x.hi[i].x, by2), b1 = decode4_fast(x.hi[i].y, by2);
-                        unsigned char *line = base + i * 512 + ((vec ^ ((line0 + 4 * i) & 7)) << 4);
-                        *reinterpret_cast<uint4 *>(line) = make_uint4(a0.x, a0.y, a1.x, a1.y);
-                        *reinterpret_cast<uint4 *>(line + F::half_bytes) = make_uint4(b0.x, b0.y, b1.x, b1.y);
+                        const uint32_t f = (__float_as_uint(scale[i]) >> 16) + (120u << 7), by2 = f | (f << 16);
+                        store(i, decode4_fast(swap ? x[i].z : x[i].x, by2), decode4_fast(swap ? x[i].w : x[i].y, by2),
+                              decode4_fast(swap ? x[i].x : x[i].z, by2), decode4_fast(swap ? x[i].y : x[i].w, by2));
                     }
                 } else {
 #pragma unroll 1
                     for (int i = 0; i < kLoads; ++i) {
-                        uint2 lo = x.lo[0], hi = x.hi[0];
-                        float f = x.scale[0];
+                        uint4 v = x[0];
+                        float f = scale[0];
 #pragma unroll
                         for (int j = 1; j < kLoads; ++j) {
-                            lo = i == j ? x.lo[j] : lo;
-                            hi = i == j ? x.hi[j] : hi;
-                            f = i == j ? x.scale[j] : f;
+                            if (i == j) v = x[j], f = scale[j];
                         }
-                        const uint2 a0 = decode4_exact(lo.x, f), a1 = decode4_exact(lo.y, f);
-                        const uint2 b0 = decode4_exact(hi.x, f), b1 = decode4_exact(hi.y, f);
-                        unsigned char *line = base + i * 512 + ((vec ^ ((line0 + 4 * i) & 7)) << 4);
-                        *reinterpret_cast<uint4 *>(line) = make_uint4(a0.x, a0.y, a1.x, a1.y);
-                        *reinterpret_cast<uint4 *>(line + F::half_bytes) = make_uint4(b0.x, b0.y, b1.x, b1.y);
+                        if (swap) v = make_uint4(v.z, v.w, v.x, v.y);
+                        store(i, decode4_exact(v.x, f), decode4_exact(v.y, f), decode4_exact(v.z, f), decode4_exact(v.w, f));
                     }
                 }
-                if (sg + 1 < kGroups) fetch(x);
+                if (sg + 1 < kGroups) fetch();
             }
             fence_proxy_async_shared();
             __syncwarp();
             if (lane == 0) mbar_arrive(&m->full[stage]);
             stage += S;
             if (stage >= F::ring) stage -= F::ring, phase ^= 1;
-            fetch(x);
+            c = (c + S) % C;
+            fetch();
         }
         chunks += total;
     }
