@@ -1,26 +1,48 @@
 // cache_attention.cu -- attention of new tokens over a paged cache, on the fifth-generation tensor cores.
 //
 // For the columns n = (row, head) of one CTA and a tile of 128 positions with rows K:
-//     S^T = K Q^T            [128 positions x 64 columns]
+//     S^T = K Q^T            [128 positions x 64 or 128 columns]
 //     P^T = exp2(S^T * scale - ref)
-//     O^T += K[:, :dv]^T P^T [dv x 64 columns]
+//     O^T += K[:, :dv]^T P^T [dv x 64 or 128 columns]
 // Positions are the M dimension of the first product and heads its N dimension, so a single token with
-// few heads wastes no part of the 128-row instruction, a thread of the softmax holds one position, and
-// the value is the key tile itself, read with the other dimension contiguous: each cache row is staged
-// once and used for both products.
+// few heads wastes no part of the 128-row instruction, a thread of the softmax holds few positions and
+// many columns, and the value is the key tile itself, read with the other dimension contiguous: each cache
+// row is staged once and used for both products.
 //
-// The sum of exponentials needs no maximum, only a reference that keeps exp2 in range.  `ref` is set from a
-// column's largest score, with room above; while no weight outgrows it a tile is taken with one vote.  Else
-// the columns' maxima are formed across the positions and the sums and accumulators are rescaled.  Sums are kept per thread (its positions) and joined at the end.
+// The sum of exponentials needs no maximum, only a reference that keeps exp2 in range.  A column's is set from
+// its largest score, with room above; while no weight outgrows it a tile is taken with one vote.  Else
+// the columns' maxima are formed across the positions and the sums and accumulators are rescaled.  Scores, sums,
+// references and accumulators are fp32; the weights are rounded to bf16 for the second product, whose other
+// operand, the value, has no more bits (the sums are of the unrounded weights: the roundings are to
+// nearest, 2^-9 of a weight at most).  Sums are kept per thread (its positions) and joined at the end in a fixed order.
 //
 // A CTA stays on its SM and takes one unit of work (rows x heads x a part of the positions) after the
-// other; its 20 warps are 8 of softmax (two groups of 4: 32 columns each), one that issues the products,
-// one that looks up the next unit, 8 that stage queries and rows, the rows in chunks of 128 columns by 128
-// positions in a ring.  A chunk is released when its part
-// of the second product is done, so the next tile's rows arrive while the rest of the product runs.
+// other.  Its warps are those of the softmax in groups of 4, one that issues the products, one that looks up
+// the next unit, two that stage queries, and those that stage rows, in chunks of 128 elements by 128 positions
+// in a ring.  A chunk is released when its part of the second product is done, or after the first where it is
+// no part of the value, so the next tile's rows arrive while the rest of the product runs.
 //
 // Few rows over long contexts are split into parts of the positions, whose sums and accumulators a
 // second kernel joins in a fixed order.
+//
+// What bounds it.  Of 512 elements one tile fills the ring beside the queries, so a tile's steps follow one
+// another: values, the next rows' way in, scores, softmax, 7300 cycles in all, of which the products'
+// 64 instructions take 3100 at their own rate.  Of 128 .. 192 elements the softmax bounds: 2200 of 2800 cycles
+// a tile, against 1800 of products.  8-bit rows: decoding them, 3000 cycles a chunk and set of warps, loads
+// included.  And one-off code: what runs once a unit is fetched from far, about 100 cycles for 8 instructions,
+// so masks, column maxima and sums are written for few instructions (the last tile's mask took 6300 cycles
+// before, the sums 5400).
+// Measured (GB300, device time; of the 1891 TFLOP/s and 6772 GB/s that plain products and copies reach):
+//   4096 rows x 64 heads over 512 selected rows of 512, bf16   393 us   612 TFLOP/s (32%)
+//   4 rows x 64 heads over 204800 positions of 512, bf16       181 us   4620 GB/s (68%)
+//   3 x 701 rows x 24 heads, 5000 positions of 192, causal     181 us   718 TFLOP/s (38%)
+//   1024 rows x 64 heads over 512 selected 8-bit rows of 512   135 us   507 TFLOP/s (27%)
+//   32 rows x 64 heads over 16384 positions of 512, 8 bits     144 us   1525 GB/s, 371 TFLOP/s (22%)
+//   1 row over 1000 positions of 128                           14.5 us  (latency: start, two lookups, 2 tiles, join)
+// Tried and slower: tiles of 64 positions (45 cycles an instruction of half the work); pairs of CTAs that share
+// a row (622 us against 385 then); TMA gathers of 4 rows (75 to 108 cycles for 512 bytes); bf16 rows through
+// registers (564 us); the next tile's rows prefetched into L2 (415 us: the copies fill the path already);
+// scores and values issued by a warp each (no change); a warp that looks up the rows for the others (448 us).
 #include <atomic>
 #include <cstddef>
 #include <cstdint>
@@ -37,7 +59,7 @@ namespace {
 constexpr int kMaxCols = 128;              // (row, head) columns of a CTA at most
 constexpr int kMaxRing = 5;
 constexpr int kValidSlots = 16;            // tiles whose validity bits are kept (more than the ring holds)
-constexpr int kUnits = 4;                  // units looked up ahead
+constexpr int kUnits = 4;                  // units known at a time
 constexpr int kMaxSplit = 64;
 // A column's reference is set 2^kHeadroom above its largest weight so far and moves when a weight reaches
 // twice the reference.  bf16 has the range of fp32, so the small weights lose nothing by it, and that
@@ -1210,7 +1232,9 @@ __global__ void __launch_bounds__(Cfg<C, N, FP8>::threads, 1) attention_kernel(c
     if (warp == F::mma_warp) tmem_dealloc(m->tmem, 512);
 }
 
-// Joins the parts of each (row, head): out = sum_p 2^(ref_p - max) o_p / sum_p 2^(ref_p - max) sum_p.
+// Joins the parts of each (row, head): out = sum_p 2^(ref_p - max) o_p / sum_p 2^(ref_p - max) sum_p.  A CTA a
+// pair, a thread 4 elements.  A few partial results a pair: launch and latency bound it, so it is launched ahead
+// of the first kernel's end.
 __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Kargs k)
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");  // launched ahead: until the parts are there
@@ -1301,7 +1325,7 @@ Plan plan_of(int64_t rows, int64_t h, int64_t d, int64_t b, int64_t positions, b
     p.items = b * p.tiles_per_seq * p.head_blocks;
     // parts: as many as keep the fewest tiles in a row, counting a part's start and end as 1.5 tiles
     const int64_t tiles = (positions + 127) / 128;
-        const int64_t sms = sm_count() > 0 ? sm_count() : 1;
+    const int64_t sms = sm_count() > 0 ? sm_count() : 1;
     p.parts = 1;
     double best = 0.0;
     for (int64_t n = 1; n <= kMaxSplit && n <= (tiles > 1 ? tiles : 1); ++n) {

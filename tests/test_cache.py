@@ -430,6 +430,46 @@ def test_rows_outside_the_mask_have_no_influence(kind, bad):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
+@pytest.mark.parametrize("h,d,dv", [(24, 192, 128), (24, 192, 192), (16, 128, 128), (16, 320, 128), (40, 384, 384),
+                                    (16, 512, 256), (64, 512, 512)])
+def test_a_row_that_is_not_finite_stays_with_the_rows_that_see_it(h, d, dv, kind):
+    # every layout of the kernel: the NaN lies in the third tile, in the value and past it
+    import gather_radix_select_gb300 as sel
+    per, ps, mp, at = 12, 16, 20, 295
+    cache, scales = make_cache(mp, ps, d, kind, 65)
+    table = make_table(1, mp, mp, 66)
+    q = make_q(per, h, d, 67)
+    end = torch.tensor([290 + i for i in range(per)], dtype=torch.int32)
+    clean = attend64(q, rows64(cache, scales), table, per, end, None, dv, 1 / 16)
+    for first in (dv - 8, 0, d - 1):
+        poisoned = cache.float()
+        poisoned[int(table[0, at // ps]), at % ps, first:] = math.nan
+        out, lse = sel.cache_attention(q, poisoned.to(cache.dtype), table, scales=scales, end=end.cuda(), dv=dv,
+                                       scale=1 / 16, return_lse=True)
+        seen = end > at
+        check_attention(out[~seen], lse[~seen], tuple(t[~seen] for t in clean))
+        assert bool(torch.isnan(out[seen].float()).all()) and bool(torch.isnan(lse[seen]).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n,where", [(1, 0), (300, 299), (300, 0), (129, 128)])
+def test_an_entry_outside_the_cache_is_flagged_wherever_it_is_in_the_list(n, where):
+    import gather_radix_select_gb300 as sel
+    cache, _ = make_cache(20, 16, 64, "bf16", 73)
+    table = make_table(1, 20, 20, 74)
+    q = make_q(2, 4, 64, 75)
+    g = torch.Generator().manual_seed(76)
+    idx = torch.randint(0, 320, (2, n), generator=g)
+    for entry, flag in ((320, 1), (-7, 0), (2 ** 31, 1), (2 ** 62, 1), (-2 ** 62, 0)):
+        idx[1, where] = entry
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        out, lse = sel.cache_attention(q, cache, table, idx=idx.cuda(), return_lse=True, err_flag=err)
+        check_attention(out, lse, attend64(q, rows64(cache, None), table, 2, None, idx, 64, 1 / 8))
+        assert int(err.item()) == flag
+
+
+@pytest.mark.gpu
 def test_positions_outside_the_cache_are_left_out_and_flagged():
     import gather_radix_select_gb300 as sel
     cache, _ = make_cache(4, 8, 64, "bf16", 71)
