@@ -22,8 +22,8 @@
 // in a ring.  A chunk is released when its part of the second product is done, or after the first where it is
 // no part of the value, so the next tile's rows arrive while the rest of the product runs.
 //
-// Few rows over long contexts are split into parts of the positions, whose sums and accumulators a
-// second kernel joins in a fixed order.
+// Of few rows over long contexts all tiles are shared out evenly among the CTAs, whatever row they are of; what a
+// row's parts come to, sums and accumulators, a second kernel joins in a fixed order.
 //
 // What bounds it.  Of 512 elements one tile fills the ring beside the queries, so a tile's steps follow one
 // another: values, the next rows' way in, scores, softmax, 7300 cycles in all, of which the products'
@@ -33,11 +33,11 @@
 // so masks, column maxima and sums are written for few instructions (the last tile's mask took 6300 cycles
 // before, the sums 5400).
 // Measured (GB300, device time; of the 1891 TFLOP/s and 6772 GB/s that plain products and copies reach):
-//   4096 rows x 64 heads over 512 selected rows of 512, bf16   393 us   612 TFLOP/s (32%)
-//   4 rows x 64 heads over 204800 positions of 512, bf16       181 us   4620 GB/s (68%)
-//   3 x 701 rows x 24 heads, 5000 positions of 192, causal     181 us   718 TFLOP/s (38%)
-//   1024 rows x 64 heads over 512 selected 8-bit rows of 512   135 us   507 TFLOP/s (27%)
-//   32 rows x 64 heads over 16384 positions of 512, 8 bits     144 us   1525 GB/s, 371 TFLOP/s (22%)
+//   4096 rows x 64 heads over 512 selected rows of 512, bf16   363 us   663 TFLOP/s (35%)
+//   4 rows x 64 heads over 204800 positions of 512, bf16       180 us   4640 GB/s (68%)
+//   3 x 701 rows x 24 heads, 5000 positions of 192, causal     184 us   708 TFLOP/s (37%)
+//   1024 rows x 64 heads over 512 selected 8-bit rows of 512   136 us   504 TFLOP/s (27%)
+//   32 rows x 64 heads over <= 16384 positions of 512, 8 bits  119 us   1850 GB/s, 450 TFLOP/s (27%)
 //   1 row over 1000 positions of 128                           14.5 us  (latency: start, two lookups, 2 tiles, join)
 // Tried and slower: tiles of 64 positions (45 cycles an instruction of half the work); pairs of CTAs that share
 // a row (622 us against 385 then); TMA gathers of 4 rows (75 to 108 cycles for 512 bytes); bf16 rows through
@@ -60,7 +60,9 @@ constexpr int kMaxCols = 128;              // (row, head) columns of a CTA at mo
 constexpr int kMaxRing = 5;
 constexpr int kValidSlots = 16;            // tiles whose validity bits are kept (more than the ring holds)
 constexpr int kUnits = 4;                  // units known at a time
-constexpr int kMaxSplit = 64;
+constexpr int kMaxItems = 512;             // items whose tiles are shared out evenly at most
+constexpr int kMaxCtas = 512;              // CTAs that share at most
+constexpr int kStart = 1;                  // tiles that an item's start counts for there
 // A column's reference is set 2^kHeadroom above its largest weight so far and moves when a weight reaches
 // twice the reference.  bf16 has the range of fp32, so the small weights lose nothing by it, and that
 // a weight is 2 or more is one bit of its bf16 exponent.
@@ -123,7 +125,7 @@ struct Unit {
     int64_t keys;            // positions, or list entries up to the last valid one
     int64_t list_end;        // exclusive end of the listed positions
     int rows, head0, heads;  // rows and heads of its columns: column = row * heads + head
-    int part;
+    int slot;                // where its sums and accumulators go; -1: it is a whole item, its outputs are written
     int lo, n;               // first tile and tiles
     int min_end, max_end;    // of its rows
     alignas(16) int end[kMaxCols];  // exclusive end of each column's row, 0 for unused columns
@@ -137,6 +139,8 @@ struct Misc {
     uint64_t unit_full[kUnits], unit_empty[kUnits];
     uint32_t tmem;
     int abort;
+    int units, item0;        // of this CTA: units, and, where tiles are shared out, the first one's item,
+    int before[kMaxItems + 1];  // tiles of the items before, where tiles are shared out
     alignas(16) float inv[kMaxCols];      // references, then 1 / sum
     alignas(16) float part[4][kMaxCols];  // maxima, then sums, of the four warps of a group
     alignas(16) uint32_t valid[kValidSlots][4];  // bit k of word w: position 32 w + k of the tile has a cache row
@@ -149,15 +153,19 @@ struct Plan {
     int heads_per_tile;  // heads of a head block
     int head_blocks;
     int64_t tiles_per_seq;
-    int64_t items;       // CTAs of one part
-    int parts;
+    int64_t items;       // row tiles x head blocks
+    int ctas;
+    int split;           // the items' tiles are shared out evenly among the CTAs, and their parts joined
 };
 
 struct Kargs {
     CacheAttnArgs a;
     Plan p;
-    float *part_o;   // [rows * h][parts][dv]
-    float2 *part_ml; // [rows * h][parts]: reference (log2), sum
+    // Where items are split: of each its first part's slot, and the first and last CTA that have one; a CTA has
+    // two slots, its first unit's and its last one's.
+    int4 *parts;
+    float *part_o;   // [2 ctas][columns][dv]
+    float2 *part_ml; // [2 ctas][columns]: reference (log2), sum
 };
 
 struct Waiter {
@@ -216,24 +224,119 @@ __device__ __forceinline__ int64_t entry(const CacheAttnArgs &a, int64_t row, in
                      : static_cast<int64_t>(__ldg(static_cast<const int32_t *>(a.idx) + off));
 }
 
-// One warp: unit u of the call.
-template <int N, int M>
-__device__ __forceinline__ void make_unit(const Kargs &k, int64_t u, Unit *w, int lane)
+// What an item is: its rows and heads.
+struct Item {
+    int64_t row0;
+    uint32_t seq;
+    int rows, head0, heads;
+};
+__device__ __forceinline__ Item item_of(const Kargs &k, uint32_t item)  // (no call has 2^31 items)
 {
-    const int64_t cap = k.a.t.max_pages * k.a.c.page_size;
-    // the last rows first: in a causal chunk they have the most positions (32-bit divisions: no call has 2^31
-    // units)
-    const uint32_t item = static_cast<uint32_t>(k.p.items) - 1 - static_cast<uint32_t>(u) / static_cast<uint32_t>(k.p.parts);
-    const int part = static_cast<int>(static_cast<uint32_t>(u) % static_cast<uint32_t>(k.p.parts));
+    Item it;
     const uint32_t tile = item / static_cast<uint32_t>(k.p.head_blocks);
     const int hb = static_cast<int>(item - tile * static_cast<uint32_t>(k.p.head_blocks));
-    const uint32_t seq = tile / static_cast<uint32_t>(k.p.tiles_per_seq);
-    const int64_t in_seq = static_cast<int64_t>(tile - seq * static_cast<uint32_t>(k.p.tiles_per_seq)) * k.p.rows_per_tile;
-    const int64_t row0 = seq * k.a.t.rows_per_seq + in_seq;
+    it.seq = tile / static_cast<uint32_t>(k.p.tiles_per_seq);
+    const int64_t in_seq = static_cast<int64_t>(tile - it.seq * static_cast<uint32_t>(k.p.tiles_per_seq)) * k.p.rows_per_tile;
     const int64_t left = k.a.t.rows_per_seq - in_seq;
-    const int rows = static_cast<int>(left < k.p.rows_per_tile ? left : k.p.rows_per_tile);
-    const int head0 = hb * k.p.heads_per_tile;
-    const int heads = min(k.p.heads_per_tile, k.a.h - head0);
+    it.row0 = it.seq * k.a.t.rows_per_seq + in_seq;
+    it.rows = static_cast<int>(left < k.p.rows_per_tile ? left : k.p.rows_per_tile);
+    it.head0 = hb * k.p.heads_per_tile;
+    it.heads = min(k.p.heads_per_tile, k.a.h - it.head0);
+    return it;
+}
+
+__device__ __forceinline__ int row_end(const Kargs &k, int64_t row)
+{
+    const int64_t cap = k.a.t.max_pages * k.a.c.page_size;
+    const int64_t v = k.a.end ? k.a.end[row] : cap;
+    return static_cast<int>(v < 0 ? 0 : (v > cap ? cap : v));
+}
+
+// The CTA's share of all tiles, [from, to) in the order of the items; with fewer tiles than CTAs the last have none.
+// (The host sees to it that tiles x CTAs stay below 2^31.)
+struct Share {
+    int from, to, ctas;  // ctas: those that have one
+};
+__device__ __forceinline__ Share share_of(int all, const Kargs &k)
+{
+    const int cta = static_cast<int>(blockIdx.x), ctas = min(k.p.ctas, all);
+    return cta < ctas ? Share{all * cta / ctas, all * (cta + 1) / ctas, ctas} : Share{all, all, ctas};
+}
+
+// What an item counts for there, of which the last row's positions end at `most`.
+template <int M>
+__device__ __forceinline__ int weight_of(const Kargs &k, int most)
+{
+    if (k.a.idx && most > 0) most = k.a.n;
+    return kStart + most / M + (most % M != 0);
+}
+
+// All threads: this CTA's units.  Where items are split, every CTA counts all items' tiles, an item's start as
+// kStart more, and takes an equal share of them.  (Parts of equal size for each row instead took 144 us for 32 rows
+// of up to 16384 8-bit positions of 512, whose lengths differ; shares take 119.)
+template <int M>
+__device__ __forceinline__ void find_units(const Kargs &k, Misc *m, int t, int threads)
+{
+    const int items = static_cast<int>(k.p.items), cta = static_cast<int>(blockIdx.x);
+    if (!k.p.split) {
+        if (t == 0) m->units = (items - cta + k.p.ctas - 1) / k.p.ctas;
+        return;
+    }
+    if (items == 1) {  // (counted with the unit: 1.2 us sooner, of 14.5 for one row over 1000 positions of 128)
+        if (t == 0) m->units = 1, m->item0 = 0;
+        return;
+    }
+    for (int i = t; i < items; i += threads) {
+        const Item it = item_of(k, static_cast<uint32_t>(i));
+        int most = 0;
+#pragma unroll 8
+        for (int r = 0; r < it.rows; ++r) most = max(most, row_end(k, it.row0 + r));
+        m->before[i + 1] = weight_of<M>(k, most);
+    }
+    if (t == 0) m->before[0] = 0;
+    __syncthreads();
+    if (t < 32) {
+        int sum = 0;
+#pragma unroll 1
+        for (int i = 0; i < items; i += 32) {
+            int v = i + t < items ? m->before[i + t + 1] : 0;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int o = __shfl_up_sync(0xffffffffu, v, d);
+                if (t >= d) v += o;
+            }
+            v += sum;
+            if (i + t < items) m->before[i + t + 1] = v;
+            sum = __shfl_sync(0xffffffffu, v, 31);
+        }
+        __syncwarp();
+        const Share s = share_of(sum, k);
+        int first = 0, upto = 0;  // items that end before the share, that start before its end
+#pragma unroll 1
+        for (int i = t; i < items; i += 32) {
+            first += m->before[i + 1] <= s.from ? 1 : 0;
+            upto += m->before[i] < s.to ? 1 : 0;
+        }
+        first = __reduce_add_sync(0xffffffffu, first);
+        upto = __reduce_add_sync(0xffffffffu, upto);
+        if (t == 0) {
+            m->item0 = first;
+            m->units = s.from < s.to ? upto - first : 0;
+        }
+    }
+}
+
+// One warp: unit u of the CTA.
+template <int N, int M>
+__device__ __forceinline__ void make_unit(const Kargs &k, const Misc *m, int u, Unit *w, int lane)
+{
+    const int64_t cap = k.a.t.max_pages * k.a.c.page_size;
+    // (whole items: the last rows first, in a causal chunk they have the most positions)
+    const int number = k.p.split ? m->item0 + u
+                                 : static_cast<int>(k.p.items) - 1 - static_cast<int>(blockIdx.x) - u * k.p.ctas;
+    const Item it = item_of(k, static_cast<uint32_t>(number));
+    const int64_t row0 = it.row0;
+    const int rows = it.rows, head0 = it.head0, heads = it.heads;
     int least = 0x7fffffff, most = 0;
 #pragma unroll
     for (int i = 0; i < N / 32; ++i) {
@@ -244,8 +347,7 @@ __device__ __forceinline__ void make_unit(const Kargs &k, int64_t u, Unit *w, in
         w->out[col] = static_cast<int>((row0 + row) * k.a.h) + head;
         w->q[col] = col < rows * heads ? (row0 + row) * k.a.q_row_stride + head * k.a.q_head_stride : -1;
         if (col < rows * heads) {
-            const int64_t v = k.a.end ? k.a.end[row0 + row] : cap;
-            e = static_cast<int>(v < 0 ? 0 : (v > cap ? cap : v));
+            e = row_end(k, row0 + row);
             least = min(least, e);
             most = max(most, e);
         }
@@ -278,15 +380,28 @@ __device__ __forceinline__ void make_unit(const Kargs &k, int64_t u, Unit *w, in
     if (lane == 0) {
         const int64_t tiles = (keys + M - 1) / M;
         w->row0 = row0;
-        w->seq = seq;
+        w->seq = it.seq;
         w->keys = keys;
         w->list_end = most;
         w->rows = rows;
         w->head0 = head0;
         w->heads = heads;
-        w->part = part;
-        w->lo = static_cast<int>(tiles * part / k.p.parts);
-        w->n = static_cast<int>(tiles * (part + 1) / k.p.parts) - w->lo;
+        int lo = 0, hi = static_cast<int>(tiles), slot = -1;
+        if (k.p.split) {
+            const int cta = static_cast<int>(blockIdx.x);
+            const bool one = k.p.items == 1;
+            const int at = one ? 0 : m->before[number], after = one ? weight_of<M>(k, most) : m->before[number + 1];
+            const int all = one ? after : m->before[k.p.items];
+            const Share s = share_of(all, k);
+            lo = max(s.from - at - kStart, 0);
+            hi = min(hi, max(min(s.to, after) - at - kStart, 0));
+            if (s.from > at || s.to < after) slot = 2 * cta + (u == 0 ? 0 : 1);
+            // (the last CTA whose share starts at or before the item's last tile)
+            if (s.from <= at) k.parts[number] = make_int4(slot, cta, (after * s.ctas - 1) / all, 0);
+        }
+        w->slot = slot;
+        w->lo = lo;
+        w->n = max(0, hi - lo);
         w->min_end = least;
         w->max_end = most;
     }
@@ -1030,8 +1145,8 @@ struct Softmax {
             const float ref = m->inv[at];
             m->inv[at] = l == 0.0f ? 0.0f : 1.0f / l;
             if (at < cols) {
-                if (k.p.parts > 1)
-                    k.part_ml[out_row(at) * k.p.parts + w.part] = make_float2(ref, l);
+                if (w.slot >= 0)
+                    k.part_ml[w.slot * N + at] = make_float2(ref, l);
                 else if (k.a.lse)
                     k.a.lse[out_row(at)] = l == 0.0f ? -INFINITY : (ref + log2f(l)) * 0.69314718055994531f;
             }
@@ -1042,7 +1157,7 @@ struct Softmax {
             tmem_fence_after();
         }
         const int vchunks = (k.a.dv + 127) >> 7;
-        if (k.p.parts > 1) {
+        if (w.slot >= 0) {
             // (a part without positions has the sum 0: its accumulators are not read)
 #pragma unroll 1
             for (int b = 0; n > 0 && b < 2 * vchunks; ++b) {
@@ -1054,7 +1169,7 @@ struct Softmax {
                 for (int c = 0; c < 2 * G; ++c) {
                     const int at = col(c);
                     if (at >= cols) continue;
-                    float *to = k.part_o + (out_row(at) * k.p.parts + w.part) * k.a.dv + e;
+                    float *to = k.part_o + static_cast<int64_t>(w.slot * N + at) * k.a.dv + e;
                     if (e < k.a.dv) to[0] = o[(c >> 1) * 4 + (c & 1)];
                     if (e + 8 < k.a.dv) to[8] = o[(c >> 1) * 4 + 2 + (c & 1)];
                 }
@@ -1119,7 +1234,6 @@ __global__ void __launch_bounds__(Cfg<C, N, FP8>::threads, 1) attention_kernel(c
     extern __shared__ __align__(1024) unsigned char smem[];
     Misc *m = reinterpret_cast<Misc *>(smem + F::misc_off);
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
-    const int64_t units = k.p.items * k.p.parts;
     if (t == 0) {
         for (int i = 0; i < F::ring; ++i) {
             mbar_init(&m->full[i], FP8 ? F::set_warps : F::load_warps * 32);
@@ -1141,10 +1255,12 @@ __global__ void __launch_bounds__(Cfg<C, N, FP8>::threads, 1) attention_kernel(c
         m->abort = 0;
     }
     if (warp == F::mma_warp) tmem_alloc(&m->tmem, 512);
+    find_units<F::M>(k, m, t, F::threads);
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
     const Waiter wait{&m->abort, k.a.err_flag};
+    const int units = m->units;
     // unit i of this CTA is in slot i mod kUnits
     auto take = [&](int i) -> const Unit * {
         wait(&m->unit_full[i % kUnits], (i / kUnits) & 1);
@@ -1155,18 +1271,35 @@ __global__ void __launch_bounds__(Cfg<C, N, FP8>::threads, 1) attention_kernel(c
         if (lane == 0) mbar_arrive(&m->unit_empty[i % kUnits]);
     };
 
-    if (warp < F::soft_warps) {
+    if (warp >= F::load_warp0) {
+        regs_to<F::load_regs, (F::load_regs > F::launch_regs)>();
+        const int set = (warp - F::load_warp0) / F::set_warps;
+        Loader<C, N, FP8> load{k, m, wait, smem, lane, (warp - F::load_warp0) % F::set_warps};
+        load.stage = set;  // (sets take the stages in turn)
+#pragma unroll 1
+        for (int i = 0; i < units; ++i) {
+            load.w = take(i);
+            if (load.w->n > 0) {
+                if (FP8)
+                    load.rows_codes(set);
+                else
+                    load.rows_bf16();
+                load.tile += load.w->n;
+            }
+            give(i);
+        }
+        cp_async_wait_all();
+    } else if (warp < F::soft_warps) {
         regs_to<F::soft_regs, (F::soft_regs > F::launch_regs)>();
         const int group = warp >> 2, quad = warp & 3;
         const uint32_t at = m->tmem + (static_cast<uint32_t>(quad * 32) << 16) + group * F::cols_per_group;
         Softmax<C, N, FP8> soft{k, m, wait, smem, group, quad, lane, at, at + C * N};
-        int i = 0;
 #pragma unroll 1
-        for (int64_t u = blockIdx.x; u < units; u += gridDim.x, ++i) {
+        for (int i = 0; i < units; ++i) {
             soft.unit(*take(i));
             give(i);
         }
-    } else if (warp < F::load_warp0) {
+    } else {
         regs_to<F::mma_regs, false>();
         if (warp == F::mma_warp) {
             Issuer<C, N, FP8> issue{m, wait};
@@ -1179,26 +1312,25 @@ __global__ void __launch_bounds__(Cfg<C, N, FP8>::threads, 1) attention_kernel(c
             issue.s_col = tm + C * N;
             issue.halves = (k.a.d + 63) >> 6;
             issue.vchunks = (k.a.dv + 127) >> 7;
-            int i = 0, loaded = 0;
+            int loaded = 0;
 #pragma unroll 1
-            for (int64_t u = blockIdx.x; u < units; u += gridDim.x, ++i) {
+            for (int i = 0; i < units; ++i) {
                 const int n = __reduce_max_sync(0xffffffffu, take(i)->n);
                 if (n > 0) issue.unit(n, loaded++ & 1);
                 give(i);
             }
         } else if (warp == F::unit_warp) {
-            int i = 0;
 #pragma unroll 1
-            for (int64_t u = blockIdx.x; u < units; u += gridDim.x, ++i) {
+            for (int i = 0; i < units; ++i) {
                 wait(&m->unit_empty[i % kUnits], ((i / kUnits) & 1) ^ 1);
-                make_unit<N, F::M>(k, u, &m->unit[i % kUnits], lane);
+                make_unit<N, F::M>(k, m, i, &m->unit[i % kUnits], lane);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&m->unit_full[i % kUnits]);
             }
         } else {
-            int i = 0, loaded = 0;
+            int loaded = 0;
 #pragma unroll 1
-            for (int64_t u = blockIdx.x; u < units; u += gridDim.x, ++i) {
+            for (int i = 0; i < units; ++i) {
                 const Unit *w = take(i);
                 if (w->n > 0) {
                     wait(&m->q_empty, (loaded++ & 1) ^ 1);
@@ -1207,63 +1339,57 @@ __global__ void __launch_bounds__(Cfg<C, N, FP8>::threads, 1) attention_kernel(c
                 give(i);
             }
         }
-    } else {
-        regs_to<F::load_regs, (F::load_regs > F::launch_regs)>();
-        const int set = (warp - F::load_warp0) / F::set_warps;
-        Loader<C, N, FP8> load{k, m, wait, smem, lane, (warp - F::load_warp0) % F::set_warps};
-        load.stage = set;  // (sets take the stages in turn)
-        int i = 0;
-#pragma unroll 1
-        for (int64_t u = blockIdx.x; u < units; u += gridDim.x, ++i) {
-            load.w = take(i);
-            if (load.w->n > 0) {
-                if (FP8)
-                    load.rows_codes(set);
-                else
-                    load.rows_bf16();
-                load.tile += load.w->n;
-            }
-            give(i);
-        }
-        cp_async_wait_all();
     }
     tmem_fence_before();
     __syncthreads();
     if (warp == F::mma_warp) tmem_dealloc(m->tmem, 512);
 }
 
-// Joins the parts of each (row, head): out = sum_p 2^(ref_p - max) o_p / sum_p 2^(ref_p - max) sum_p.  A CTA a
-// pair, a thread 4 elements.  A few partial results a pair: launch and latency bound it, so it is launched ahead
+// Joins the parts of each column: out = sum_p 2^(ref_p - max) o_p / sum_p 2^(ref_p - max) sum_p.  A CTA a
+// column, a thread 4 elements.  A few partial results each: launch and latency bound it, so it is launched ahead
 // of the first kernel's end.
 __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Kargs k)
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");  // launched ahead: until the parts are there
-    const int64_t item = blockIdx.x;
-    const int parts = k.p.parts, dv = k.a.dv;
-    const float2 *ml = k.part_ml + item * parts;
+    const int N = k.p.cols, dv = k.a.dv;
+    const uint32_t item = blockIdx.x / static_cast<uint32_t>(N);
+    const int col = static_cast<int>(blockIdx.x - item * static_cast<uint32_t>(N));
+    const int4 at = k.parts[item];
+    if (at.x < 0) return;  // a whole one
+    const Item it = item_of(k, item);
+    if (col >= it.rows * it.heads) return;
+    const int row = col / it.heads;
+    const int64_t out = (it.row0 + row) * k.a.h + it.head0 + col - row * it.heads;
+    auto slot = [&](int p) { return static_cast<int64_t>(p == 0 ? at.x : 2 * (at.y + p)) * N + col; };
+    __shared__ float2 part[kMaxCtas];  // reference and sum, then factor and sum, of each part
+    const int parts = at.z - at.y + 1;
+    for (int p = threadIdx.x; p < parts; p += 128) part[p] = k.part_ml[slot(p)];
+    __syncthreads();
     float top = -INFINITY;
-    for (int p = 0; p < parts; ++p) {
-        const float2 v = ml[p];
-        if (v.y != 0.0f) top = fmaxf(top, v.x);
+    for (int p = 0; p < parts; ++p) top = fmaxf(top, part[p].y != 0.0f ? part[p].x : -INFINITY);
+    __syncthreads();
+    for (int p = threadIdx.x; p < parts; p += 128) {
+        const float2 v = part[p];
+        part[p].x = v.y == 0.0f ? 0.0f : v.x == top ? 1.0f : exp2_approx(v.x - top);
     }
+    __syncthreads();
     float sum = 0.0f;
     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     const int e = threadIdx.x * 4;
+#pragma unroll 4
     for (int p = 0; p < parts; ++p) {
-        const float2 v = ml[p];
-        if (v.y == 0.0f) continue;
-        const float f = v.x == top ? 1.0f : exp2_approx(v.x - top);
-        sum += f * v.y;
-        if (e < dv) {
-            const float4 o = *reinterpret_cast<const float4 *>(k.part_o + (item * parts + p) * dv + e);
-            acc.x += f * o.x, acc.y += f * o.y, acc.z += f * o.z, acc.w += f * o.w;
-        }
+        const float f = part[p].x;
+        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        // (a part whose sum is 0 has written no accumulators)
+        if (e < dv && part[p].y != 0.0f) o = *reinterpret_cast<const float4 *>(k.part_o + slot(p) * dv + e);
+        sum += f * part[p].y;
+        acc.x += f * o.x, acc.y += f * o.y, acc.z += f * o.z, acc.w += f * o.w;
     }
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
     if (e < dv)
-        *reinterpret_cast<uint2 *>(k.a.out + item * dv + e) =
+        *reinterpret_cast<uint2 *>(k.a.out + out * dv + e) =
             make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-    if (threadIdx.x == 0 && k.a.lse) k.a.lse[item] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
+    if (threadIdx.x == 0 && k.a.lse) k.a.lse[out] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
 }
 
 // The current device's SMs, asked for once a device.
@@ -1298,8 +1424,7 @@ cudaError_t launch(const Kargs &k, cudaStream_t s)
         if (e != cudaSuccess) return e;
         set.fetch_or(bit, std::memory_order_relaxed);
     }
-    const int64_t units = k.p.items * k.p.parts, sms = sm_count();
-    attention_kernel<C, N, FP8><<<static_cast<unsigned>(units < sms ? units : sms), F::threads, smem, s>>>(k);
+    attention_kernel<C, N, FP8><<<static_cast<unsigned>(k.p.ctas), F::threads, smem, s>>>(k);
     return cudaGetLastError();
 }
 
@@ -1323,24 +1448,22 @@ Plan plan_of(int64_t rows, int64_t h, int64_t d, int64_t b, int64_t positions, b
     p.rows_per_tile = static_cast<int>(fit < per ? fit : per);
     p.tiles_per_seq = (per + p.rows_per_tile - 1) / p.rows_per_tile;
     p.items = b * p.tiles_per_seq * p.head_blocks;
-    // parts: as many as keep the fewest tiles in a row, counting a part's start and end as 1.5 tiles
-    const int64_t tiles = (positions + 127) / 128;
+    // Few items: their tiles are shared out, where that leaves the fewest tiles in a row, counting a part's start
+    // and end as 1.5 tiles and the join as 1.
+    const int64_t tiles = positions > 128 ? (positions + 127) / 128 : 1;
     const int64_t sms = sm_count() > 0 ? sm_count() : 1;
-    p.parts = 1;
-    double best = 0.0;
-    for (int64_t n = 1; n <= kMaxSplit && n <= (tiles > 1 ? tiles : 1); ++n) {
-        const int64_t waves = (p.items * n + sms - 1) / sms;
-        const double cost = static_cast<double>(waves) * (static_cast<double>((tiles + n - 1) / n) + 1.5) + (n > 1 ? 1.0 : 0.0);
-        if (n == 1 || cost < best) {
-            best = cost;
-            p.parts = static_cast<int>(n);
-        }
-        if (p.items * n > 2 * sms) break;
-    }
+    const int64_t waves = (p.items + sms - 1) / sms;
+    const double whole = static_cast<double>(waves) * (static_cast<double>(tiles) + 1.5);
+    const int64_t all = p.items * (tiles + kStart), most = sms < kMaxCtas ? sms : kMaxCtas, ctas = all < most ? all : most;
+    const double shared = static_cast<double>((all + ctas - 1) / ctas) + 1.5 + 1.0;
+    p.split = p.items <= kMaxItems && p.items < 2 * sms && all < 0x7fffffff / (sms + 1) && shared < whole;
+    p.ctas = static_cast<int>(p.split ? ctas : p.items < sms ? p.items : sms);
     return p;
 }
 
-size_t part_bytes(int64_t items, int parts) { return static_cast<size_t>((items * parts * 8 + 255) / 256 * 256); }
+size_t rounded(size_t n) { return (n + 255) / 256 * 256; }
+size_t parts_bytes(const Plan &p) { return rounded(static_cast<size_t>(p.items) * sizeof(int4)); }
+size_t ml_bytes(const Plan &p) { return rounded(static_cast<size_t>(2) * p.ctas * p.cols * sizeof(float2)); }
 
 }  // namespace
 
@@ -1348,8 +1471,8 @@ size_t cache_attention_workspace(int64_t rows, int64_t h, int64_t d, int64_t dv,
                                  bool idx_given)
 {
     const Plan p = plan_of(rows, h, d, b, positions, idx_given);
-    if (p.parts == 1) return 0;
-    return part_bytes(rows * h, p.parts) + static_cast<size_t>(rows * h) * p.parts * dv * 4;
+    if (!p.split) return 0;
+    return parts_bytes(p) + ml_bytes(p) + static_cast<size_t>(2) * p.ctas * p.cols * dv * sizeof(float);
 }
 
 cudaError_t launch_cache_attention(const CacheAttnArgs &a, cudaStream_t s)
@@ -1357,9 +1480,11 @@ cudaError_t launch_cache_attention(const CacheAttnArgs &a, cudaStream_t s)
     Kargs k{};
     k.a = a;
     k.p = plan_of(a.rows, a.h, a.d, a.rows / a.t.rows_per_seq, a.idx ? a.n : a.t.max_pages * a.c.page_size, a.idx != nullptr);
-    if (k.p.parts > 1) {
-        k.part_ml = static_cast<float2 *>(a.ws);
-        k.part_o = reinterpret_cast<float *>(static_cast<unsigned char *>(a.ws) + part_bytes(a.rows * a.h, k.p.parts));
+    if (k.p.split) {
+        unsigned char *ws = static_cast<unsigned char *>(a.ws);
+        k.parts = reinterpret_cast<int4 *>(ws);
+        k.part_ml = reinterpret_cast<float2 *>(ws + parts_bytes(k.p));
+        k.part_o = reinterpret_cast<float *>(ws + parts_bytes(k.p) + ml_bytes(k.p));
     }
     cudaError_t e;
     if (k.p.cols == 128)
@@ -1368,9 +1493,9 @@ cudaError_t launch_cache_attention(const CacheAttnArgs &a, cudaStream_t s)
         e = a.d <= 128 ? launch<1, 64>(k, s) : launch<2, 64>(k, s);
     else
         e = a.d <= 384 ? launch<3, 64>(k, s) : launch<4, 64>(k, s);
-    if (e != cudaSuccess || k.p.parts == 1) return e;
+    if (e != cudaSuccess || !k.p.split) return e;
     cudaLaunchConfig_t at = {};
-    at.gridDim = dim3(static_cast<unsigned>(a.rows * a.h));
+    at.gridDim = dim3(static_cast<unsigned>(k.p.items * k.p.cols));
     at.blockDim = dim3(128);
     at.stream = s;
     cudaLaunchAttribute ahead;

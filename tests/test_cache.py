@@ -368,6 +368,30 @@ def test_attention_over_long_contexts(b, per, d):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
+@pytest.mark.parametrize("h,d,ends", [
+    (64, 128, [0, 1, 130, 7000, 3]),          # most have next to nothing
+    (96, 64, [6000, 0, 0, 5999]),             # two blocks of heads a row
+    (8, 512, [5, 2000]),
+    (40, 256, [0, 0, 0]),                     # nothing at all
+    (16, 192, [128 * i for i in range(40)]),  # more rows than can have many parts
+])
+def test_unequal_contexts(h, d, ends, kind):
+    import gather_radix_select_gb300 as sel
+    b, ps = len(ends), 64
+    mp = -(-max(max(ends), 1) // ps) + 9
+    cache, scales = make_cache(300, ps, d, kind, 45)
+    g = torch.Generator().manual_seed(46)
+    table = torch.randint(0, 300, (b, mp), generator=g, dtype=torch.int32).cuda()  # (sequences may share pages)
+    q = make_q(b, h, d, 47)
+    end = torch.tensor(ends, dtype=torch.int32)
+    out, lse = sel.cache_attention(q, cache, table, scales=scales, end=end.cuda(), return_lse=True)
+    check_attention(out, lse, attend64(q, rows64(cache, scales), table, 1, end, None, d, 1 / math.sqrt(d)))
+    again, _ = sel.cache_attention(q, cache, table, scales=scales, end=end.cuda())
+    assert torch.equal(out.view(torch.int16), again.view(torch.int16))
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("spread", [0.0, 30.0, -30.0])
 def test_attention_when_the_maximum_moves(spread):
     # scores that climb (or fall) along the positions: the running maximum moves at every tile, or never
