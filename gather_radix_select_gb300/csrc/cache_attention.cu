@@ -33,12 +33,12 @@
 // so masks, column maxima and sums are written for few instructions (the last tile's mask took 6300 cycles
 // before, the sums 5400).
 // Measured (GB300, device time; of the 1891 TFLOP/s and 6772 GB/s that plain products and copies reach):
-//   4096 rows x 64 heads over 512 selected rows of 512, bf16   363 us   663 TFLOP/s (35%)
-//   4 rows x 64 heads over 204800 positions of 512, bf16       180 us   4640 GB/s (68%)
+//   4096 rows x 64 heads over 512 selected rows of 512, bf16   364 us   660 TFLOP/s (35%)
+//   4 rows x 64 heads over 204800 positions of 512, bf16       170 us   4930 GB/s (73%)
 //   3 x 701 rows x 24 heads, 5000 positions of 192, causal     184 us   708 TFLOP/s (37%)
 //   1024 rows x 64 heads over 512 selected 8-bit rows of 512   136 us   504 TFLOP/s (27%)
-//   32 rows x 64 heads over <= 16384 positions of 512, 8 bits  119 us   1850 GB/s, 450 TFLOP/s (27%)
-//   1 row over 1000 positions of 128                           14.5 us  (latency: start, two lookups, 2 tiles, join)
+//   32 rows x 64 heads over <= 16384 positions of 512, 8 bits  120 us   1830 GB/s, 446 TFLOP/s (27%)
+//   1 row over 1000 positions of 128                           12.6 us  (latency: start, lookups, a tile, join)
 // Tried and slower: tiles of 64 positions (45 cycles an instruction of half the work); pairs of CTAs that share
 // a row (622 us against 385 then); TMA gathers of 4 rows (75 to 108 cycles for 512 bytes); bf16 rows through
 // registers (564 us); the next tile's rows prefetched into L2 (415 us: the copies fill the path already);
@@ -282,7 +282,7 @@ __device__ __forceinline__ void find_units(const Kargs &k, Misc *m, int t, int t
         if (t == 0) m->units = (items - cta + k.p.ctas - 1) / k.p.ctas;
         return;
     }
-    if (items == 1) {  // (counted with the unit: 1.2 us sooner, of 14.5 for one row over 1000 positions of 128)
+    if (items == 1) {  // (counted with the unit: 1.2 us sooner)
         if (t == 0) m->units = 1, m->item0 = 0;
         return;
     }
@@ -1346,50 +1346,61 @@ __global__ void __launch_bounds__(Cfg<C, N, FP8>::threads, 1) attention_kernel(c
 }
 
 // Joins the parts of each column: out = sum_p 2^(ref_p - max) o_p / sum_p 2^(ref_p - max) sum_p.  A CTA a
-// column, a thread 4 elements.  A few partial results each: launch and latency bound it, so it is launched ahead
-// of the first kernel's end.
-__global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Kargs k)
+// column; `V` threads have 4 elements of a part each, and the CTA's groups of as many take every groups-th part, so
+// that few loads follow one another: their latency bounds it (4 rows x 64 heads of 512 over 204800 positions, 39
+// parts a column: 178 us with one group of 128 threads, 169.5 with four).  Launched ahead of the first kernel's end.
+constexpr int kJoinThreads = 512;
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ Kargs k, int V)
 {
+    __shared__ float2 part[kMaxCtas];  // reference and sum, then factor and sum, of each part
+    __shared__ float4 partial[kJoinThreads];
     asm volatile("griddepcontrol.wait;" ::: "memory");  // launched ahead: until the parts are there
-    const int N = k.p.cols, dv = k.a.dv;
+    const int N = k.p.cols, dv = k.a.dv, t = threadIdx.x, lane = t & 31;
     const uint32_t item = blockIdx.x / static_cast<uint32_t>(N);
     const int col = static_cast<int>(blockIdx.x - item * static_cast<uint32_t>(N));
     const int4 at = k.parts[item];
     if (at.x < 0) return;  // a whole one
     const Item it = item_of(k, item);
     if (col >= it.rows * it.heads) return;
-    const int row = col / it.heads;
-    const int64_t out = (it.row0 + row) * k.a.h + it.head0 + col - row * it.heads;
     auto slot = [&](int p) { return static_cast<int64_t>(p == 0 ? at.x : 2 * (at.y + p)) * N + col; };
-    __shared__ float2 part[kMaxCtas];  // reference and sum, then factor and sum, of each part
     const int parts = at.z - at.y + 1;
-    for (int p = threadIdx.x; p < parts; p += 128) part[p] = k.part_ml[slot(p)];
+    for (int p = t; p < parts; p += blockDim.x) part[p] = k.part_ml[slot(p)];
     __syncthreads();
-    float top = -INFINITY;
-    for (int p = 0; p < parts; ++p) top = fmaxf(top, part[p].y != 0.0f ? part[p].x : -INFINITY);
-    __syncthreads();
-    for (int p = threadIdx.x; p < parts; p += 128) {
-        const float2 v = part[p];
-        part[p].x = v.y == 0.0f ? 0.0f : v.x == top ? 1.0f : exp2_approx(v.x - top);
-    }
-    __syncthreads();
-    float sum = 0.0f;
+    float top = -INFINITY, sum = 0.0f;  // (each warp for itself, in the same order)
+    for (int p = lane; p < parts; p += 32) top = fmaxf(top, part[p].y != 0.0f ? part[p].x : -INFINITY);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    auto factor = [&](float2 v) { return v.y == 0.0f ? 0.0f : v.x == top ? 1.0f : exp2_approx(v.x - top); };
+    for (int p = lane; p < parts; p += 32) sum += factor(part[p]) * part[p].y;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    const int groups = blockDim.x / V, group = t / V, e = (t - group * V) * 4;
     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    const int e = threadIdx.x * 4;
 #pragma unroll 4
-    for (int p = 0; p < parts; ++p) {
-        const float f = part[p].x;
+    for (int p = group; p < parts; p += groups) {
+        const float2 v = part[p];
         float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         // (a part whose sum is 0 has written no accumulators)
-        if (e < dv && part[p].y != 0.0f) o = *reinterpret_cast<const float4 *>(k.part_o + slot(p) * dv + e);
-        sum += f * part[p].y;
+        if (e < dv && v.y != 0.0f) o = *reinterpret_cast<const float4 *>(k.part_o + slot(p) * dv + e);
+        const float f = factor(v);
         acc.x += f * o.x, acc.y += f * o.y, acc.z += f * o.z, acc.w += f * o.w;
     }
+    if (groups > 1) {
+        partial[t] = acc;
+        __syncthreads();
+        if (group > 0) return;
+        for (int g = 1; g < groups; ++g) {
+            const float4 o = partial[g * V + t];
+            acc.x += o.x, acc.y += o.y, acc.z += o.z, acc.w += o.w;
+        }
+    }
+    const int row = col / it.heads;
+    const int64_t out = (it.row0 + row) * k.a.h + it.head0 + col - row * it.heads;
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
     if (e < dv)
         *reinterpret_cast<uint2 *>(k.a.out + out * dv + e) =
             make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-    if (threadIdx.x == 0 && k.a.lse) k.a.lse[out] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
+    if (t == 0 && k.a.lse) k.a.lse[out] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
 }
 
 // The current device's SMs, asked for once a device.
@@ -1494,16 +1505,23 @@ cudaError_t launch_cache_attention(const CacheAttnArgs &a, cudaStream_t s)
     else
         e = a.d <= 384 ? launch<3, 64>(k, s) : launch<4, 64>(k, s);
     if (e != cudaSuccess || !k.p.split) return e;
+    // groups for half of the parts that a column has, as long as all threads are resident at once (2048 columns of
+    // 6 parts: 119 us with the first kernel by one group, 121 by two, 127 by four)
+    int vecs = 32;
+    while (vecs * 4 < a.dv) vecs *= 2;
+    const int64_t columns = k.p.items * k.p.cols, parts = (k.p.ctas + k.p.items) / k.p.items, sms = sm_count();
+    int threads = vecs;
+    while (threads < kJoinThreads && threads / vecs * 2 < parts && columns * threads * 2 <= 2048 * sms) threads *= 2;
     cudaLaunchConfig_t at = {};
     at.gridDim = dim3(static_cast<unsigned>(k.p.items * k.p.cols));
-    at.blockDim = dim3(128);
+    at.blockDim = dim3(static_cast<unsigned>(threads));
     at.stream = s;
     cudaLaunchAttribute ahead;
     ahead.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     ahead.val.programmaticStreamSerializationAllowed = 1;
     at.attrs = &ahead;
     at.numAttrs = 1;
-    return cudaLaunchKernelEx(&at, join_kernel, k);
+    return cudaLaunchKernelEx(&at, join_kernel, k, vecs);
 }
 
 }  // namespace sel
