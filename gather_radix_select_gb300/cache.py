@@ -174,7 +174,7 @@ def cache_gather(cache: torch.Tensor, page_table: torch.Tensor, idx: torch.Tenso
     err = _flag(err_flag, dev)
 
     def call(s):
-        to = cache.new_empty((rows, n, d), dtype=torch.bfloat16) if out is None else out
+        to = torch.empty((rows, n, d), dtype=torch.bfloat16, device=dev) if out is None else out
         return _native.load().sel_cache_gather(
             c, page_table.data_ptr(), b, m, table_stride, idx.data_ptr(), _IDX[idx.dtype], rows, n, idx_stride,
             to.data_ptr(), err, s), to
@@ -231,8 +231,8 @@ def cache_attention(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tens
 
     def call(s):
         lib = _native.load()
-        to = q.new_empty((rows, h, max(dv, 0))) if out is None else out
-        lse = q.new_empty((rows, h), dtype=torch.float32) if return_lse else None
+        to = torch.empty((rows, h, max(dv, 0)), dtype=torch.bfloat16, device=dev) if out is None else out
+        lse = torch.empty((rows, h), dtype=torch.float32, device=dev) if return_lse else None
         need = _scratch_bytes(dev.index, rows, h, d, dv, b, m, c.page_size, idx_ptr is not None, n)
         ws = _scratch(need, q, s) if need else None
         return lib.sel_cache_attention(
