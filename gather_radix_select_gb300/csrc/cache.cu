@@ -17,7 +17,7 @@ namespace {
 
 constexpr int kWriteThreads = 128;
 constexpr int kWriteLanes = 16;   // lanes of one run of 128 elements, 8 elements each
-constexpr int kGatherPairs = 128; // positions of one row handled by one CTA at most
+constexpr int kGatherPairs = 128; // positions handled by one CTA at most
 
 __device__ __forceinline__ void load8(const void *x, bool bf16, int64_t at, float v[8])
 {
@@ -135,21 +135,29 @@ __device__ __forceinline__ uint4 decode8(uint2 codes, float scale)
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// One CTA per run of positions of one row: their cache rows are found once, then copied 16 output
-// bytes a lane, four vectors under way at a time.  The output's bytes bound it: 4096 rows x 512 positions of 128
+// One CTA per run of positions, of whatever rows: their cache rows are found once, then copied 16 output
+// bytes a lane, four vectors under way at a time.  (By runs within a row short lists left most of a CTA idle:
+// 26334 rows x 7 positions of 256 took 45.5 us, now 19.)  The output's bytes bound it: 4096 rows x 512 positions of 128
 // elements (537 MB out, the cache's rows from L2) take 77.8 us, 6.9 TB/s; 1024 x 512 positions of 8-bit rows of
 // 512 (as many bytes out) 83.8 us.
 template <bool FP8>
-__global__ void __launch_bounds__(kGatherThreads) cache_gather_kernel(const CacheGatherArgs a)
+__global__ void __launch_bounds__(kGatherThreads, 8) cache_gather_kernel(const CacheGatherArgs a)
 {
     __shared__ int64_t s_row[kGatherPairs];    // element offset of the cache row, -1: none
     __shared__ int64_t s_scale[kGatherPairs];
-    const int64_t row = blockIdx.x / a.ctas_per_row;
-    const int64_t j0 = (blockIdx.x - row * a.ctas_per_row) * a.pairs;
-    const int np = static_cast<int>(a.n - j0 < a.pairs ? a.n - j0 : a.pairs);
-    const int64_t seq = row / a.t.rows_per_seq;
+    const int64_t total = a.rows * a.n, first = static_cast<int64_t>(blockIdx.x) * a.pairs;
+    const int np = static_cast<int>(total - first < a.pairs ? total - first : a.pairs);
     for (int i = threadIdx.x; i < np; i += kGatherThreads) {
-        const int64_t off = row * a.idx_row_stride + j0 + i;
+        const int64_t at_i = first + i;
+        int64_t row, seq;
+        if (total >> 32 == 0) {  // the common case, without the 64-bit divisions
+            row = static_cast<uint32_t>(at_i) / static_cast<uint32_t>(a.n);
+            seq = static_cast<uint32_t>(row) / static_cast<uint32_t>(a.t.rows_per_seq);
+        } else {
+            row = at_i / a.n;
+            seq = row / a.t.rows_per_seq;
+        }
+        const int64_t off = row * a.idx_row_stride + (at_i - row * a.n);
         int64_t p = a.idx_i64 ? static_cast<const int64_t *>(a.idx)[off]
                               : static_cast<int64_t>(static_cast<const int32_t *>(a.idx)[off]);
         p = p < 0 ? 0 : p;
@@ -166,10 +174,10 @@ __global__ void __launch_bounds__(kGatherThreads) cache_gather_kernel(const Cach
     __syncthreads();
     const int vpr = static_cast<int>(a.c.d >> 3);
     const int vsh = (vpr & (vpr - 1)) == 0 ? __ffs(vpr) - 1 : -1;
-    uint4 *out = reinterpret_cast<uint4 *>(a.out + (row * a.n + j0) * a.c.d);
-    const int total = np * vpr;
+    uint4 *out = reinterpret_cast<uint4 *>(a.out + first * a.c.d);
+    const int vecs = np * vpr;
     constexpr int U = 4;
-    for (int t0 = threadIdx.x; t0 < total; t0 += U * kGatherThreads) {
+    for (int t0 = threadIdx.x; t0 < vecs; t0 += U * kGatherThreads) {
         uint4 v[U];
         float sc[U];
 #pragma unroll
@@ -177,7 +185,7 @@ __global__ void __launch_bounds__(kGatherThreads) cache_gather_kernel(const Cach
             const int t = t0 + u * kGatherThreads;
             v[u] = make_uint4(0u, 0u, 0u, 0u);
             sc[u] = 0.0f;
-            if (t < total) {
+            if (t < vecs) {
                 const int jj = vsh >= 0 ? (t >> vsh) : t / vpr;
                 const int c = t - jj * vpr;
                 const int64_t r = s_row[jj];
@@ -196,9 +204,17 @@ __global__ void __launch_bounds__(kGatherThreads) cache_gather_kernel(const Cach
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int t = t0 + u * kGatherThreads;
-            if (t < total) __stcs(out + t, FP8 ? decode8(make_uint2(v[u].x, v[u].y), sc[u]) : v[u]);
+            if (t < vecs) __stcs(out + t, FP8 ? decode8(make_uint2(v[u].x, v[u].y), sc[u]) : v[u]);
         }
     }
+}
+
+// log2(n), or -1 when n is no power of two (or 2^32 and more).
+int shift_of(int64_t n)
+{
+    int s = 0;
+    while (s < 31 && (int64_t{1} << s) < n) ++s;
+    return (int64_t{1} << s) == n ? s : -1;
 }
 
 }  // namespace
@@ -209,11 +225,6 @@ cudaError_t launch_cache_write(const CacheWriteArgs &a, cudaStream_t s)
     const int64_t items = a.tokens * runs, grid = (items * kWriteLanes + kWriteThreads - 1) / kWriteThreads;
     if (grid <= 0) return cudaSuccess;
     if (items > 0x7fffffffLL / kWriteLanes) return cudaErrorInvalidValue;
-    auto shift_of = [](int64_t n) {
-        int s = 0;
-        while (s < 31 && (int64_t{1} << s) < n) ++s;
-        return (int64_t{1} << s) == n ? s : -1;
-    };
     cache_write_kernel<<<static_cast<unsigned>(grid), kWriteThreads, 0, s>>>(
         a, static_cast<uint32_t>(runs), shift_of(runs), shift_of(a.c.page_size), static_cast<uint32_t>(items));
     return cudaGetLastError();
@@ -225,11 +236,11 @@ cudaError_t launch_cache_gather(const CacheGatherArgs &a_in, cudaStream_t s)
     // few positions: fewer a CTA, down to 8, so that there are 4 CTAs for every SM (16 rows x 512 positions of 512
     // elements: 6.3 us, with 128 positions a CTA 10.4)
     const int64_t sms = device_sm_count() > 0 ? device_sm_count() : 1;
+    const int64_t total = a.rows * a.n;
     int64_t pairs = kGatherPairs;
-    while (pairs > 8 && a.rows * ((a.n + pairs - 1) / pairs) < 4 * sms) pairs /= 2;
+    while (pairs > 8 && (total + pairs - 1) / pairs < 4 * sms) pairs /= 2;
     a.pairs = static_cast<int32_t>(pairs);
-    a.ctas_per_row = static_cast<int32_t>((a.n + pairs - 1) / pairs);
-    const int64_t grid = a.rows * a.ctas_per_row;
+    const int64_t grid = (total + pairs - 1) / pairs;
     if (grid <= 0) return cudaSuccess;
     if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
     if (a.c.scales)

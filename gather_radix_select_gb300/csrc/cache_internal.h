@@ -46,7 +46,7 @@ struct CacheGatherArgs {
     int64_t rows, n, idx_row_stride;
     uint16_t *out;
     int32_t *err_flag;
-    int32_t pairs, ctas_per_row;  // set by the launcher
+    int32_t pairs;  // positions of a CTA, set by the launcher
 };
 
 struct CacheAttnArgs {
