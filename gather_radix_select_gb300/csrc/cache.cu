@@ -137,9 +137,10 @@ __device__ __forceinline__ uint4 decode8(uint2 codes, float scale)
 
 // One CTA per run of positions, of whatever rows: their cache rows are found once, then copied 16 output
 // bytes a lane, four vectors under way at a time.  (By runs within a row short lists left most of a CTA idle:
-// 26334 rows x 7 positions of 256 took 45.5 us, now 19.)  The output's bytes bound it: 4096 rows x 512 positions of 128
-// elements (537 MB out, the cache's rows from L2) take 77.8 us, 6.9 TB/s; 1024 x 512 positions of 8-bit rows of
-// 512 (as many bytes out) 83.8 us.
+// 26334 rows x 7 positions of 256 took 45.5 us, now 19.  8 CTAs an SM: with the 36 registers that
+// 8-bit rows take unbounded, 16 x 512 positions would be more than one wave, 7.5 against 6.3 us.)
+// The output's bytes bound it: 4096 rows x 512 positions of 128 elements (537 MB out, the cache's rows from L2)
+// take 78 us, 6.9 TB/s; 1024 x 512 positions of 8-bit rows of 512 (as many bytes out) 83.5 us.
 template <bool FP8>
 __global__ void __launch_bounds__(kGatherThreads, 8) cache_gather_kernel(const CacheGatherArgs a)
 {

@@ -265,6 +265,22 @@ def test_gathered_rows(kind, shape, itype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
+@pytest.mark.parametrize("b,per,n", [(7, 300, 3), (3, 1, 129), (1, 5000, 1), (2, 61, 67)])
+def test_gathered_runs_cross_rows(kind, b, per, n):
+    import gather_radix_select_gb300 as sel
+    cache, scales = make_cache(40, 12, 48, kind, 37)
+    table = make_table(b, 5, 40, 38)
+    g = torch.Generator().manual_seed(39)
+    wide = torch.randint(0, 60, (b * per, n + 3), generator=g, dtype=torch.int32)
+    out = sel.cache_gather(cache, table, wide.cuda()[:, :n], scales=scales)
+    idx = wide[:, :n].long()
+    seq = (torch.arange(b * per) // per)[:, None].expand(-1, n)
+    want = rows64(cache, scales)[table.cpu().long()[seq, idx // 12], idx % 12]
+    assert torch.equal(out.cpu().double(), want)
+
+
+@pytest.mark.gpu
 def test_gathered_positions_outside_give_zero_rows_and_the_flag():
     import gather_radix_select_gb300 as sel
     cache, _ = make_cache(3, 4, 16, "bf16", 1)
