@@ -124,7 +124,7 @@ struct Unit {
     int64_t row0, seq;
     int64_t keys;            // positions, or list entries up to the last valid one
     int64_t list_end;        // exclusive end of the listed positions
-    int rows, head0, heads;  // rows and heads of its columns: column = row * heads + head
+    int rows, heads;         // of its columns: column = row * heads + head
     int slot;                // where its sums and accumulators go; -1: it is a whole item, its outputs are written
     int lo, n;               // first tile and tiles
     int min_end, max_end;    // of its rows
@@ -139,7 +139,7 @@ struct Misc {
     uint64_t unit_full[kUnits], unit_empty[kUnits];
     uint32_t tmem;
     int abort;
-    int units, item0;        // of this CTA: units, and, where tiles are shared out, the first one's item,
+    int units, item0;        // of this CTA: units, and, where tiles are shared out, the first one's item
     int before[kMaxItems + 1];  // tiles of the items before, where tiles are shared out
     alignas(16) float inv[kMaxCols];      // references, then 1 / sum
     alignas(16) float part[4][kMaxCols];  // maxima, then sums, of the four warps of a group
@@ -384,7 +384,6 @@ __device__ __forceinline__ void make_unit(const Kargs &k, const Misc *m, int u, 
         w->keys = keys;
         w->list_end = most;
         w->rows = rows;
-        w->head0 = head0;
         w->heads = heads;
         int lo = 0, hi = static_cast<int>(tiles), slot = -1;
         if (k.p.split) {
@@ -564,7 +563,6 @@ struct Loader {
         const int line0 = lw * kPos + (lane >> 4);
         const uint32_t to = smem_addr(smem) + (vec >> 3) * F::half_bytes + line0 * 128;
         const int halves = (d + 63) >> 6;
-        constexpr int V = kVecs < 8 ? kVecs : 8;
         int64_t pos = position(1);
         Place at = page_of(position(0));
 #pragma unroll 1
@@ -573,11 +571,9 @@ struct Loader {
             note(it, cur);
             at = page_of(pos);
             pos = position(it + 2);
-            int64_t row[V];
-            if (kVecs <= 8) {
+            int64_t row[kVecs];
 #pragma unroll
-                for (int i = 0; i < V; ++i) row[i] = __shfl_sync(0xffffffffu, cur.row, 2 * i + (lane >> 4));
-            }
+            for (int i = 0; i < kVecs; ++i) row[i] = __shfl_sync(0xffffffffu, cur.row, 2 * i + (lane >> 4));
 #pragma unroll 1
             for (int c = 0; c < C; ++c) {
                 const int stage = at_ring.stage(c);
@@ -587,10 +583,9 @@ struct Loader {
                 const bool used = c * 2 + (vec >> 3) < halves;
 #pragma unroll
                 for (int i = 0; i < kVecs; ++i) {
-                    const int64_t r = kVecs <= 8 ? row[i & (V - 1)] : __shfl_sync(0xffffffffu, cur.row, 2 * i + (lane >> 4));
-                    const bool ok = e < d && r >= 0;
+                    const bool ok = e < d && row[i] >= 0;
                     if (used)
-                        cp_async16(base + i * 256 + (((vec & 7) ^ ((line0 + 2 * i) & 7)) << 4), data + (ok ? r + e : 0),
+                        cp_async16(base + i * 256 + (((vec & 7) ^ ((line0 + 2 * i) & 7)) << 4), data + (ok ? row[i] + e : 0),
                                    ok ? 16u : 0u);
                 }
                 cp_async_arrive(&m->full[stage]);
