@@ -59,6 +59,7 @@ namespace {
 constexpr int kMaxCols = 128;              // (row, head) columns of a CTA at most
 constexpr int kMaxRing = 5;
 constexpr int kValidSlots = 16;            // tiles whose validity bits are kept (more than the ring holds)
+constexpr int kNoted = 8;                  // tiles whose validity bits may be under way (the ring holds 5, lookups are 2 ahead)
 constexpr int kUnits = 4;                  // units known at a time
 constexpr int kMaxItems = 512;             // items whose tiles are shared out evenly at most
 constexpr int kMaxCtas = 512;              // CTAs that share at most
@@ -92,7 +93,8 @@ struct Cfg {
     static constexpr bool own = wide && C == 2 && !FP8;
     static constexpr int ring = own ? 5 : wide && C == 1 ? 3 : (C == 1 ? 5 : 4);
     static constexpr int ring_bytes = own ? 4 * chunk_bytes : ring * chunk_bytes;
-    static constexpr int own0 = 3;  // places of the first chunk
+    static constexpr int own0 = 3, own1 = 2;  // places of the first chunk, of the second
+    static_assert(!own || own0 + own1 == ring, "");
     static __device__ __forceinline__ int place(int stage) { return stage * chunk_bytes - (own && stage > own0 ? half_bytes : 0); }
     static constexpr int pbufs = C == 1 || (C == 2 && !wide) ? 2 : 1;
     static constexpr bool ahead = ring >= 2 * C;  // the next tile's scores before this one's values
@@ -115,7 +117,7 @@ struct Cfg {
     static constexpr int soft_regs = wide ? (FP8 ? 88 : 96) : FP8 ? 96 : 64;
     static constexpr int mma_regs = wide && !FP8 ? 32 : 40;
     static constexpr int load_regs = wide ? (FP8 ? 88 : 40) : FP8 ? 64 : 96;
-    static_assert(ring >= C && ring <= kMaxRing, "");
+    static_assert(ring >= C && ring <= kMaxRing && ring / C + 2 < kNoted && kNoted <= kValidSlots, "");
     static_assert(32 * soft_warps * soft_regs + 128 * mma_regs + 32 * load_warps * load_regs <= threads * launch_regs, "");
 };
 
@@ -136,6 +138,7 @@ struct Unit {
 
 struct Misc {
     uint64_t full[kMaxRing], empty[kMaxRing], s_full[2], s_empty[2], p_full[2], pv_done[2], q_full, q_empty;
+    uint64_t noted[kNoted];  // validity bits of a tile: the scores' barriers say nothing of them
     uint64_t unit_full[kUnits], unit_empty[kUnits];
     uint32_t tmem;
     int abort;
@@ -541,7 +544,8 @@ struct Loader {
                     at.page * k.a.c.scale_page_stride + at.in_page * k.a.c.scale_row_stride};
     }
 
-    // This warp's validity bits of tile i of the unit.
+    // This warp's validity bits of tile i of the unit.  (They have a barrier of their own: of the staged chunks only
+    // the copies are waited for, which orders no ordinary store before them.)
     __device__ __forceinline__ void note(int i, const Rows &r) const
     {
         const uint32_t bits = __ballot_sync(0xffffffffu, r.row >= 0);
@@ -551,6 +555,7 @@ struct Loader {
                 to[lw] = bits;
             else
                 reinterpret_cast<uint16_t *>(to)[lw] = static_cast<uint16_t>(bits);
+            mbar_arrive(&m->noted[(tile + i) & (kNoted - 1)]);
         }
     }
 
@@ -1013,10 +1018,20 @@ struct Softmax {
             for (int r = 0; r < 2; ++r)
                 if (((mask.valid >> (2 * h + r)) & 1u) && !(fabsf(x[h][2 * r]) < INFINITY)) dirty |= 1u << (2 * h + r);
         if (!bar_any(5, F::soft_warps * 32, dirty != 0)) return 0;
-        const int stage0 = static_cast<int>((static_cast<int64_t>(tile) * C) % F::ring);
+        // chunk c of the tile: its place in the ring, and how often that was filled before
+        auto stage_of = [&](int c) {
+            if (!F::own) return static_cast<int>((static_cast<int64_t>(tile) * C + c) % F::ring);
+            return c ? F::own0 + tile % F::own1 : tile % F::own0;
+        };
+        auto fills_of = [&](int c) {
+            if (!F::own) return static_cast<int>((static_cast<int64_t>(tile) * C + c) / F::ring);
+            return c ? tile / F::own1 : tile / F::own0;
+        };
+        // (the chunks are read here: the scores' barrier speaks for the products alone)
+#pragma unroll 1
+        for (int c = 0; c * 128 < k.a.dv; ++c) wait(&m->full[stage_of(c)], fills_of(c) & 1);
         auto unit16 = [&](int at, int e) {
-            const int c = e >> 7;
-            const int stage = !F::own ? (stage0 + c) % F::ring : c ? F::own0 + tile % (F::ring - F::own0) : tile % F::own0;
+            const int stage = stage_of(e >> 7);
             return smem + F::place(stage) + ((e >> 6) & 1) * F::half_bytes + at * 128 +
                    ((((e >> 3) & 7) ^ (at & 7)) << 4);
         };
@@ -1051,6 +1066,7 @@ struct Softmax {
             mask.pos0 = (w.lo + it) * F::M;
             mask.ends = w.end;
             mask.edges = !k.a.idx && mask.pos0 + F::M > w.min_end && w.min_end < w.max_end;
+            wait(&m->noted[tile & (kNoted - 1)], (tile / kNoted) & 1);
             wait(&m->s_full[buf], (tile >> 1) & 1);
             tmem_fence_after();
             const uint4 words = *reinterpret_cast<const uint4 *>(m->valid[tile & (kValidSlots - 1)]);
@@ -1240,6 +1256,7 @@ __global__ void __launch_bounds__(Cfg<C, N, FP8>::threads, 1) attention_kernel(c
             mbar_init(&m->p_full[i], F::soft_warps);
             mbar_init(&m->pv_done[i], 1);
         }
+        for (int i = 0; i < kNoted; ++i) mbar_init(&m->noted[i], F::set_warps);
         for (int i = 0; i < kUnits; ++i) {
             mbar_init(&m->unit_full[i], 1);
             mbar_init(&m->unit_empty[i], F::soft_warps + 3 + F::load_warps);
