@@ -68,6 +68,7 @@ constexpr int kStart = 1;                  // tiles that an item's start counts 
 // twice the reference.  bf16 has the range of fp32, so the small weights lose nothing by it, and that
 // a weight is 2 or more is one bit of its bf16 exponent.
 constexpr float kHeadroom = 24.0f;
+constexpr float kNoReference = -3.4028235e38f;  // of a column without a score above -inf: any such score outgrows it
 constexpr long long kWaitCycles = 4000000000LL;  // about 2 s
 constexpr uint32_t kSuspend = 1000;
 constexpr int32_t kTimeout = 5;            // SEL_ETIMEOUT
@@ -937,9 +938,9 @@ struct Softmax {
         return __shfl_sync(0xffffffffu, v, (c << (G == 4 ? 2 : 3)) | (lane & 3));
     }
 
-    // Weights outgrow their columns' references, or there are none yet (not `started`): new references, sums
-    // and, where there are `products`, accumulators brought to them.
-    __device__ __forceinline__ void move_references(const float x[H][X], bool started, bool products)
+    // Weights outgrow their columns' references: new references, sums and accumulators brought to them.  (The
+    // unit's `first` tile sets the references, there is nothing to bring along.)
+    __device__ __forceinline__ void move_references(const float x[H][X], bool first)
     {
         float top[2 * G];
 #pragma unroll
@@ -956,33 +957,31 @@ struct Softmax {
         bar_sync(1 + group, 128);
         const float most = fmaxf(fmaxf(m->part[0][at], m->part[1][at]), fmaxf(m->part[2][at], m->part[3][at]));
         const float was = -pick(neg);
-        // (a column without positions so far will have none later: it keeps the reference 0)
-        const float now = most == -INFINITY ? was : started ? fmaxf(was, most + kHeadroom) : most + kHeadroom;
+        // (a column without a score above -inf so far, for whatever reason, may still get one: it stays without)
+        const float now = most == -INFINITY ? was : fmaxf(was, most + kHeadroom);
 #pragma unroll
         for (int g = 0; g < G; ++g) neg[g] = make_float2(-from_own(now, 2 * g), -from_own(now, 2 * g + 1));
-        if (!started) return;  // (nothing to rescale)
+        if (first) return;
         const float by = was == now ? 1.0f : exp2_approx(was - now);
 #pragma unroll
         for (int g = 0; g < G; ++g) {
             sum[g].x *= from_own(by, 2 * g);
             sum[g].y *= from_own(by, 2 * g + 1);
         }
-        if (products) {
-            wait(&m->pv_done[(tile - 1) & 1], ((tile - 1) >> 1) & 1);
-            tmem_fence_after();
-            const int vchunks = (k.a.dv + 127) >> 7;
+        wait(&m->pv_done[(tile - 1) & 1], ((tile - 1) >> 1) & 1);
+        tmem_fence_after();
+        const int vchunks = (k.a.dv + 127) >> 7;
 #pragma unroll 1
-            for (int c = 0; c < 2 * vchunks; ++c) {
-                const uint32_t at = o_tm + (c >> 1) * N + (static_cast<uint32_t>((c & 1) * 16) << 16);
-                float o[X];
-                tmem_ld<G>(at, o);
-                tmem_wait_ld();
+        for (int c = 0; c < 2 * vchunks; ++c) {
+            const uint32_t at = o_tm + (c >> 1) * N + (static_cast<uint32_t>((c & 1) * 16) << 16);
+            float o[X];
+            tmem_ld<G>(at, o);
+            tmem_wait_ld();
 #pragma unroll
-                for (int i = 0; i < X; ++i) o[i] *= from_own(by, 2 * (i >> 2) + (i & 1));
-                tmem_st<G>(at, o);
-            }
-            tmem_wait_st();
+            for (int i = 0; i < X; ++i) o[i] *= from_own(by, 2 * (i >> 2) + (i & 1));
+            tmem_st<G>(at, o);
         }
+        tmem_wait_st();
     }
 
     // A tile's weights 2^(score * scale - reference), two positions by G pairs of columns a block, as bf16
@@ -1057,7 +1056,6 @@ struct Softmax {
     __device__ __forceinline__ void tiles(const Unit &w)
     {
         const int n = w.n;
-        bool started = false;  // a tile with a position has been there
         const uint32_t vshift = line(0, 0) & 31;  // the thread's first position within its word of validity bits
 #pragma unroll 1
         for (int it = 0; it < n; ++it, ++tile) {
@@ -1082,22 +1080,17 @@ struct Softmax {
                 if (mask.edges) dirty = take_out(x, mask);
                 mask_all(x, mask, dirty);
             }
-            // the first tile with a position sets the references, a later one moves them when a weight outgrows
-            // its own
-            bool set = false;
-            if (!started) {
-                set = started = (words.x | words.y | words.z | words.w) != 0;
-                if (started) move_references(x, false, false);
-            }
+            // the first tile sets the references, a later one moves them when a weight outgrows its own
+            if (it == 0) move_references(x, true);
             uint32_t out[H][2 * G];
             float2 to[G];
 #pragma unroll
             for (int g = 0; g < G; ++g) to[g] = sum[g];
             const bool over = weights(x, out, to);
-            if (!set && bar_any(1 + group, 128, over)) {
+            if (it > 0 && bar_any(1 + group, 128, over)) {
                 load_scores(x, buf);  // (not kept: registers)
                 if (!whole) mask_all(x, mask, dirty);
-                move_references(x, true, it > 0);
+                move_references(x, false);
 #pragma unroll
                 for (int g = 0; g < G; ++g) to[g] = sum[g];
                 weights(x, out, to);
@@ -1135,7 +1128,7 @@ struct Softmax {
         auto out_row = [&](int c) { return static_cast<int64_t>(w.out[c]); };
 #pragma unroll
         for (int g = 0; g < G; ++g) {
-            neg[g] = make_float2(0.0f, 0.0f);
+            neg[g] = make_float2(-kNoReference, -kNoReference);
             sum[g] = make_float2(0.0f, 0.0f);
         }
         tiles(w);
