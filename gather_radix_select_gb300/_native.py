@@ -64,6 +64,7 @@ SIGNATURES = {
     "sel_cache_gather": (_int, [_cache_p, _vp, _i64, _i64, _i64, _vp, _int, _i64, _i64, _i64, _vp, _vp, _vp]),
     "sel_cache_attention": (_int, [_vp, _i64, _i64, _i64, _i64, _cache_p, _vp, _i64, _i64, _i64, _vp, _vp, _int,
                                    _i64, _i64, _i64, ctypes.c_float, _vp, _vp, _vp, ctypes.c_size_t, _vp, _vp]),
+    "sel_cache_set_wait_limit": (_int, [_i64]),
     "sel_cache_attention_workspace_size": (ctypes.c_size_t, [_i64, _i64, _i64, _i64, _i64, _i64, _i64, _int, _i64]),
 }
 

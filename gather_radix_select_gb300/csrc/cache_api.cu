@@ -140,6 +140,12 @@ int sel_cache_gather(const sel_cache *cache, const int32_t *page_table, int64_t 
     return status_of(sel::launch_cache_gather(a, static_cast<cudaStream_t>(stream)));
 }
 
+int sel_cache_set_wait_limit(int64_t cycles)
+{
+    sel::set_cache_wait_cycles(cycles);
+    return SEL_OK;
+}
+
 size_t sel_cache_attention_workspace_size(int64_t rows, int64_t h, int64_t d, int64_t dv, int64_t b, int64_t max_pages,
                                           int64_t page_size, int idx_given, int64_t n)
 {

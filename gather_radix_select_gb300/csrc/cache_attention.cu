@@ -69,7 +69,7 @@ constexpr int kStart = 1;                  // tiles that an item's start counts 
 // a weight is 2 or more is one bit of its bf16 exponent.
 constexpr float kHeadroom = 24.0f;
 constexpr float kNoReference = -3.4028235e38f;  // of a column without a score above -inf: any such score outgrows it
-constexpr long long kWaitCycles = 4000000000LL;  // about 2 s
+constexpr long long kWaitCycles = 4000000000LL;  // about 2 s: no wait of a working kernel takes a thousandth of it
 constexpr uint32_t kSuspend = 1000;
 constexpr int32_t kTimeout = 5;            // SEL_ETIMEOUT
 
@@ -141,6 +141,7 @@ struct Misc {
     uint64_t full[kMaxRing], empty[kMaxRing], s_full[2], s_empty[2], p_full[2], pv_done[2], q_full, q_empty;
     uint64_t noted[kNoted];  // validity bits of a tile: the scores' barriers say nothing of them
     uint64_t unit_full[kUnits], unit_empty[kUnits];
+    uint64_t drained;        // every product is done
     uint32_t tmem;
     int abort;
     int units, item0;        // of this CTA: units, and, where tiles are shared out, the first one's item
@@ -170,32 +171,43 @@ struct Kargs {
     int4 *parts;
     float *part_o;   // [2 ctas][columns][dv]
     float2 *part_ml; // [2 ctas][columns]: reference (log2), sum
+    long long wait_cycles;  // after which a wait gives up
 };
 
+// Waits that end.  One that has waited for `limit` cycles gives up and says so in `abort`, after which every wait of
+// the CTA that is not over by itself gives up too, and in err_flag (SEL_ETIMEOUT).  What follows is this:
+//  - a unit's loops have counts of their own and addresses that do not depend on what was waited for, so whoever has
+//    a unit ends it, and its results are NaN;
+//  - a unit that did not come is not looked at (its fields may be anything): the role leaves.  The softmax's
+//    warps, which meet at barriers, leave together, and put NaN where the results of the units left would go;
+//  - the unit warp leaves instead of writing over a unit that may be in use;
+//  - the tensor memory is freed once the products issued so far are done.
 struct Waiter {
     volatile int *abort;
     int32_t *err;
-    // Waits until the phase of `parity` has completed.  After about 2 s without that, or once another
-    // thread gave up, it returns all the same: every loop has a fixed count, so the CTA ends, with
-    // SEL_ETIMEOUT in err_flag.
-    __device__ __forceinline__ void operator()(uint64_t *bar, int parity) const
+    long long limit;
+    // Whether the phase of `parity` has completed; the same for the whole warp.
+    __device__ __forceinline__ bool operator()(uint64_t *bar, int parity) const
     {
-        if (!mbar_try_wait(bar, static_cast<uint32_t>(parity), kSuspend)) slow(bar, parity);
-        __syncwarp();  // (whole warps wait: none of their lanes falls behind by a phase)
+        const bool over = mbar_try_wait(bar, static_cast<uint32_t>(parity), kSuspend) || slow(bar, parity);
+        return __all_sync(0xffffffffu, over);  // (none of the warp's lanes falls behind by a phase)
     }
-    __device__ __forceinline__ void slow(uint64_t *bar, int parity) const
+    __device__ __forceinline__ bool slow(uint64_t *bar, int parity) const
     {
         const long long t0 = clock64();
         while (!mbar_try_wait(bar, static_cast<uint32_t>(parity), kSuspend)) {
-            if (*abort) return;
-            if (clock64() - t0 > kWaitCycles) {
+            if (*abort) return false;
+            if (clock64() - t0 > limit) {
                 *abort = 1;
                 if (err) atomicCAS(err, 0, kTimeout);
-                return;
+                return false;
             }
         }
+        return true;
     }
 };
+
+__device__ __forceinline__ float quiet_nan() { return __int_as_float(0x7fffffff); }
 
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
 {
@@ -275,6 +287,29 @@ __device__ __forceinline__ int weight_of(const Kargs &k, int most)
     return kStart + most / M + (most % M != 0);
 }
 
+// Where the sums and accumulators of the CTA's unit u go, an item's [at, after) of all `all` tiles; -1: nowhere, it is
+// the whole item.
+__device__ __forceinline__ int slot_of(const Share &s, int u, int at, int after)
+{
+    return s.from > at || s.to < after ? 2 * static_cast<int>(blockIdx.x) + (u == 0 ? 0 : 1) : -1;
+}
+
+// The item's entry for the join, by the CTA that has its start.
+__device__ __forceinline__ void note_parts(const Kargs &k, const Share &s, int number, int u, int at, int after, int all)
+{
+    // (the last CTA whose share starts at or before the item's last tile)
+    if (s.from <= at)
+        k.parts[number] = make_int4(slot_of(s, u, at, after), static_cast<int>(blockIdx.x), (after * s.ctas - 1) / all, 0);
+}
+
+// The item that the CTA's unit u is, or is part of.  (Whole items: the last rows first, in a causal chunk they have
+// the most positions.)
+__device__ __forceinline__ int item_number(const Kargs &k, const Misc *m, int u)
+{
+    return k.p.split ? m->item0 + u
+                     : static_cast<int>(k.p.items) - 1 - static_cast<int>(blockIdx.x) - u * k.p.ctas;
+}
+
 // All threads: this CTA's units.  Where items are split, every CTA counts all items' tiles, an item's start as
 // kStart more, and takes an equal share of them.  (Parts of equal size for each row instead took 144 us for 32 rows
 // of up to 16384 8-bit positions of 512, whose lengths differ; shares take 119.)
@@ -323,10 +358,13 @@ __device__ __forceinline__ void find_units(const Kargs &k, Misc *m, int t, int t
         }
         first = __reduce_add_sync(0xffffffffu, first);
         upto = __reduce_add_sync(0xffffffffu, upto);
+        const int units = s.from < s.to ? upto - first : 0;
         if (t == 0) {
             m->item0 = first;
-            m->units = s.from < s.to ? upto - first : 0;
+            m->units = units;
         }
+        // (here, where nothing is waited for: the join reads them whatever becomes of the units)
+        for (int u = t; u < units; u += 32) note_parts(k, s, first + u, u, m->before[first + u], m->before[first + u + 1], sum);
     }
 }
 
@@ -335,9 +373,7 @@ template <int N, int M>
 __device__ __forceinline__ void make_unit(const Kargs &k, const Misc *m, int u, Unit *w, int lane)
 {
     const int64_t cap = k.a.t.max_pages * k.a.c.page_size;
-    // (whole items: the last rows first, in a causal chunk they have the most positions)
-    const int number = k.p.split ? m->item0 + u
-                                 : static_cast<int>(k.p.items) - 1 - static_cast<int>(blockIdx.x) - u * k.p.ctas;
+    const int number = item_number(k, m, u);
     const Item it = item_of(k, static_cast<uint32_t>(number));
     const int64_t row0 = it.row0;
     const int rows = it.rows, head0 = it.head0, heads = it.heads;
@@ -391,16 +427,14 @@ __device__ __forceinline__ void make_unit(const Kargs &k, const Misc *m, int u, 
         w->heads = heads;
         int lo = 0, hi = static_cast<int>(tiles), slot = -1;
         if (k.p.split) {
-            const int cta = static_cast<int>(blockIdx.x);
             const bool one = k.p.items == 1;
             const int at = one ? 0 : m->before[number], after = one ? weight_of<M>(k, most) : m->before[number + 1];
             const int all = one ? after : m->before[k.p.items];
             const Share s = share_of(all, k);
             lo = max(s.from - at - kStart, 0);
             hi = min(hi, max(min(s.to, after) - at - kStart, 0));
-            if (s.from > at || s.to < after) slot = 2 * cta + (u == 0 ? 0 : 1);
-            // (the last CTA whose share starts at or before the item's last tile)
-            if (s.from <= at) k.parts[number] = make_int4(slot, cta, (after * s.ctas - 1) / all, 0);
+            slot = slot_of(s, u, at, after);
+            if (one) note_parts(k, s, number, u, at, after, all);
         }
         w->slot = slot;
         w->lo = lo;
@@ -876,7 +910,7 @@ struct Softmax {
             for (int h = 0; h < H; ++h)
 #pragma unroll
                 for (int i = 0; i < X; ++i)
-                    if ((dirty >> (2 * h + ((i >> 1) & 1))) & 1u) x[h][i] = __int_as_float(0x7fffffff);
+                    if ((dirty >> (2 * h + ((i >> 1) & 1))) & 1u) x[h][i] = quiet_nan();
         }
         // a position against the ends: its offset from the thread's first, or past every end without a row
         int at[H][2];
@@ -1160,6 +1194,15 @@ struct Softmax {
             wait(&m->pv_done[(tile - 1) & 1], ((tile - 1) >> 1) & 1);
             tmem_fence_after();
         }
+        // (the unit's last wait is behind it: one that gave up leaves no result of the unit)
+        const bool lost = *wait.abort != 0;
+        if (lost && quad == 0 && lane < W && group * W + lane < cols) {
+            const int at = group * W + lane;
+            if (w.slot >= 0)
+                k.part_ml[w.slot * N + at] = make_float2(0.0f, quiet_nan());
+            else if (k.a.lse)
+                k.a.lse[out_row(at)] = quiet_nan();
+        }
         const int vchunks = (k.a.dv + 127) >> 7;
         if (w.slot >= 0) {
             // (a part without positions has the sum 0: its accumulators are not read)
@@ -1185,7 +1228,7 @@ struct Softmax {
         unsigned char *stage = smem + F::p_off + (group * 4 + quad) * (W * 64);
         float2 inv[G];
 #pragma unroll
-        for (int g = 0; g < G; ++g) inv[g] = make_float2(m->inv[col(2 * g)], m->inv[col(2 * g + 1)]);
+        for (int g = 0; g < G; ++g) inv[g] = lost ? make_float2(quiet_nan(), quiet_nan()) : make_float2(m->inv[col(2 * g)], m->inv[col(2 * g + 1)]);
         uint16_t *to[W / 8];  // the vectors this thread writes; null: unused
 #pragma unroll
         for (int i = 0; i < W / 8; ++i) {
@@ -1226,7 +1269,28 @@ struct Softmax {
             }
             __syncwarp();
         }
-        bar_sync(5, F::soft_warps * 32);  // the next unit's P covers every warp's staging
+    }
+
+    // The units from `u` on have not come: NaN where their results would go.
+    __device__ __forceinline__ void give_up(int u, int units) const
+    {
+        constexpr int kThreads = F::soft_warps * 32;
+        const int t = (group * 4 + quad) * 32 + lane;
+#pragma unroll 1
+        for (; u < units; ++u) {
+            const Item it = item_of(k, static_cast<uint32_t>(item_number(k, m, u)));
+#pragma unroll 1
+            for (int r = 0; r < it.rows; ++r) {
+                const int64_t first = (it.row0 + r) * k.a.h + it.head0;
+#pragma unroll 1
+                for (int i = t; i < it.heads * k.a.dv; i += kThreads) k.a.out[first * k.a.dv + i] = 0x7fff;
+#pragma unroll 1
+                for (int i = t; k.a.lse && i < it.heads; i += kThreads) k.a.lse[first + i] = quiet_nan();
+            }
+#pragma unroll 1
+            for (int i = t; k.p.split && i < N; i += kThreads)
+                k.part_ml[(2 * static_cast<int>(blockIdx.x) + (u == 0 ? 0 : 1)) * N + i] = make_float2(0.0f, quiet_nan());
+        }
     }
 };
 
@@ -1256,6 +1320,7 @@ __global__ void __launch_bounds__(Cfg<C, N, FP8>::threads, 1) attention_kernel(c
         }
         mbar_init(&m->q_full, 2);
         mbar_init(&m->q_empty, 1);
+        mbar_init(&m->drained, 1);
         fence_mbar_init();
         m->abort = 0;
     }
@@ -1264,12 +1329,11 @@ __global__ void __launch_bounds__(Cfg<C, N, FP8>::threads, 1) attention_kernel(c
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
-    const Waiter wait{&m->abort, k.a.err_flag};
+    const Waiter wait{&m->abort, k.a.err_flag, k.wait_cycles};
     const int units = m->units;
-    // unit i of this CTA is in slot i mod kUnits
+    // unit i of this CTA is in slot i mod kUnits; null: it did not come
     auto take = [&](int i) -> const Unit * {
-        wait(&m->unit_full[i % kUnits], (i / kUnits) & 1);
-        return &m->unit[i % kUnits];
+        return wait(&m->unit_full[i % kUnits], (i / kUnits) & 1) ? &m->unit[i % kUnits] : nullptr;
     };
     auto give = [&](int i) {
         __syncwarp();
@@ -1284,6 +1348,7 @@ __global__ void __launch_bounds__(Cfg<C, N, FP8>::threads, 1) attention_kernel(c
 #pragma unroll 1
         for (int i = 0; i < units; ++i) {
             load.w = take(i);
+            if (!load.w) break;
             if (load.w->n > 0) {
                 if (FP8)
                     load.rows_codes(set);
@@ -1301,7 +1366,13 @@ __global__ void __launch_bounds__(Cfg<C, N, FP8>::threads, 1) attention_kernel(c
         Softmax<C, N, FP8> soft{k, m, wait, smem, group, quad, lane, at, at + C * N};
 #pragma unroll 1
         for (int i = 0; i < units; ++i) {
-            soft.unit(*take(i));
+            const Unit *w = take(i);
+            // (also: the unit's P covers what every warp staged for the one before)
+            if (bar_any(5, F::soft_warps * 32, w == nullptr)) {
+                soft.give_up(i, units);
+                break;
+            }
+            soft.unit(*w);
             give(i);
         }
     } else {
@@ -1320,14 +1391,20 @@ __global__ void __launch_bounds__(Cfg<C, N, FP8>::threads, 1) attention_kernel(c
             int loaded = 0;
 #pragma unroll 1
             for (int i = 0; i < units; ++i) {
-                const int n = __reduce_max_sync(0xffffffffu, take(i)->n);
+                const Unit *w = take(i);
+                if (!w) break;
+                const int n = __reduce_max_sync(0xffffffffu, w->n);
                 if (n > 0) issue.unit(n, loaded++ & 1);
                 give(i);
             }
+            // no product is under way when the tensor memory is freed.  (This wait has the whole limit, whoever gave up.)
+            if (elect_one()) umma_commit(&m->drained);
+            int none = 0;
+            Waiter{&none, k.a.err_flag, kWaitCycles}(&m->drained, 0);
         } else if (warp == F::unit_warp) {
 #pragma unroll 1
             for (int i = 0; i < units; ++i) {
-                wait(&m->unit_empty[i % kUnits], ((i / kUnits) & 1) ^ 1);
+                if (!wait(&m->unit_empty[i % kUnits], ((i / kUnits) & 1) ^ 1)) break;
                 make_unit<N, F::M>(k, m, i, &m->unit[i % kUnits], lane);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&m->unit_full[i % kUnits]);
@@ -1337,6 +1414,7 @@ __global__ void __launch_bounds__(Cfg<C, N, FP8>::threads, 1) attention_kernel(c
 #pragma unroll 1
             for (int i = 0; i < units; ++i) {
                 const Unit *w = take(i);
+                if (!w) break;
                 if (w->n > 0) {
                     wait(&m->q_empty, (loaded++ & 1) ^ 1);
                     load_queries<C, N, FP8>(k, w, m, smem, warp - F::unit_warp - 1, lane);
@@ -1491,10 +1569,18 @@ size_t cache_attention_workspace(int64_t rows, int64_t h, int64_t d, int64_t dv,
     return parts_bytes(p) + ml_bytes(p) + static_cast<size_t>(2) * p.ctas * p.cols * dv * sizeof(float);
 }
 
+static std::atomic<long long> g_wait_cycles{kWaitCycles};
+
+void set_cache_wait_cycles(long long cycles)
+{
+    g_wait_cycles.store(cycles < 0 ? kWaitCycles : cycles, std::memory_order_relaxed);
+}
+
 cudaError_t launch_cache_attention(const CacheAttnArgs &a, cudaStream_t s)
 {
     Kargs k{};
     k.a = a;
+    k.wait_cycles = g_wait_cycles.load(std::memory_order_relaxed);
     k.p = plan_of(a.rows, a.h, a.d, a.rows / a.t.rows_per_seq, a.idx ? a.n : a.t.max_pages * a.c.page_size, a.idx != nullptr);
     if (k.p.split) {
         unsigned char *ws = static_cast<unsigned char *>(a.ws);

@@ -71,6 +71,9 @@ cudaError_t launch_cache_write(const CacheWriteArgs &a, cudaStream_t s);
 cudaError_t launch_cache_gather(const CacheGatherArgs &a, cudaStream_t s);
 cudaError_t launch_cache_attention(const CacheAttnArgs &a, cudaStream_t s);
 
+// Cycles after which a wait of the attention kernel gives up, from the next call on; negative: the usual ones.
+void set_cache_wait_cycles(long long cycles);
+
 // Workspace bytes of an attention call; launches nothing.
 size_t cache_attention_workspace(int64_t rows, int64_t h, int64_t d, int64_t dv, int64_t b, int64_t positions,
                                  bool idx_given);

@@ -101,6 +101,9 @@ SEL_API int sel_cache_gather(const sel_cache *cache, const int32_t *page_table, 
  * Positions past the page table, or whose page is not in [0, pages), are left
  * out and set *err_flag = SEL_EINVAL.  Sums and the softmax are in fp32; the
  * weights are rounded to bf16 for the product with the values.
+ * The waits between a CTA's warps end: one that runs out (after about 2 s, where
+ * microseconds are usual) sets *err_flag = SEL_ETIMEOUT, and the rows whose
+ * results were lost by it hold NaN in out and lse, with or without an err_flag.
  * SEL_EUNSUPPORTED: d > SEL_CACHE_ATTN_MAX_D, rows * h > 2^31 - 1, or
  * n or max_pages * page_size > 2^31 - 256. */
 SEL_API int sel_cache_attention(const void *q, int64_t rows, int64_t h, int64_t q_row_stride, int64_t q_head_stride,
@@ -114,6 +117,11 @@ SEL_API int sel_cache_attention(const void *q, int64_t rows, int64_t h, int64_t 
  * over several CTAs.  0 on invalid arguments. */
 SEL_API size_t sel_cache_attention_workspace_size(int64_t rows, int64_t h, int64_t d, int64_t dv, int64_t b,
                                                   int64_t max_pages, int64_t page_size, int idx_given, int64_t n);
+
+/* Test hook: GPU clock cycles after which a wait of sel_cache_attention gives
+ * up, for the calls that follow, in the whole process; negative: the usual
+ * 4e9.  Always SEL_OK. */
+SEL_API int sel_cache_set_wait_limit(int64_t cycles);
 
 #ifdef __cplusplus
 }
