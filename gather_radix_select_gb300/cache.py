@@ -111,21 +111,6 @@ def _scratch_bytes(device_index, rows, h, d, dv, b, max_pages, page_size, idx_gi
                                                                  n))
 
 
-_SCRATCH: dict = {}
-
-
-def _scratch(nbytes, like, raw_stream):
-    """A scratch buffer of >= nbytes kept for each stream (calls on one stream never overlap), or, while a graph is
-    captured, one of its own."""
-    if torch.cuda.is_current_stream_capturing():
-        return like.new_empty(nbytes, dtype=torch.uint8)
-    key = (like.device.index, raw_stream)
-    buf = _SCRATCH.get(key)
-    if buf is None or buf.shape[0] < nbytes:
-        buf = _SCRATCH[key] = like.new_empty(max(nbytes, 1 << 20), dtype=torch.uint8)
-    return buf
-
-
 def cache_write(x: torch.Tensor, cache: torch.Tensor, slots: torch.Tensor, *, scales: torch.Tensor | None = None,
                 err_flag: torch.Tensor | None = None, stream=None) -> None:
     """Writes rows ``x`` [tokens, d] (bf16 or fp32, rows may be strided) into ``cache`` at ``slots``
@@ -234,7 +219,9 @@ def cache_attention(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tens
         to = torch.empty((rows, h, max(dv, 0)), dtype=torch.bfloat16, device=dev) if out is None else out
         lse = torch.empty((rows, h), dtype=torch.float32, device=dev) if return_lse else None
         need = _scratch_bytes(dev.index, rows, h, d, dv, b, m, c.page_size, idx_ptr is not None, n)
-        ws = _scratch(need, q, s) if need else None
+        # Scratch of the call's own, from the stream's pool: two launches pass data through it, and another thread's
+        # call on the same stream may come between them.
+        ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
         return lib.sel_cache_attention(
             q.data_ptr(), rows, h, q_row if rows > 1 else h * d, q_head if h > 1 else d, c, page_table.data_ptr(),
             b, m, table_stride, None if end is None else end.data_ptr(), idx_ptr, idx_type, n, idx_stride, dv,
