@@ -62,9 +62,6 @@ def _stream(device, stream):
     return ctypes.c_void_p(s.cuda_stream)
 
 
-_WORKSPACES: dict = {}
-
-
 def workspace_size(dtype: torch.dtype, rows: int, cols: int, k: int, device=None) -> int:
     """Scratch bytes a top-k call of this shape needs on ``device`` (0 for most shapes)."""
     with torch.cuda.device(device if device is not None else torch.cuda.current_device()):
@@ -115,15 +112,12 @@ def get_tuning() -> dict:
 
 
 def _workspace(nbytes: int, device, stream):
-    """A scratch buffer of >= nbytes, cached per (device, stream) (calls on one stream never overlap)."""
+    """Scratch of a call's own, from the pool of its stream.  (A call enqueues more than one operation that uses it, its
+    counters' reset before the kernel, and another thread's call on the stream may come between them.)"""
     if nbytes == 0:
         return None, 0
-    key = (device.index, stream.cuda_stream)
-    buf = _WORKSPACES.get(key)
-    if buf is None or buf.numel() < nbytes:
-        buf = torch.empty(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
-        _WORKSPACES[key] = buf
-    return buf, buf.numel()
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device), nbytes
 
 
 def _padded_rows(rows: int, k: int, dtype: torch.dtype, device) -> torch.Tensor:
@@ -207,7 +201,7 @@ def topk(x: torch.Tensor, k: int, *, end: torch.Tensor | None = None, sorted_ind
     ``output_val`` are optional caller-owned [rows, >=k] buffers (row strides
     a multiple of the output alignment); results go to their first k columns.
     ``workspace`` (uint8 CUDA tensor) is only needed when few wide rows are
-    split over several CTAs; by default a cached buffer is used.
+    split over several CTAs; by default one is allocated for the call.
     """
     _check_x(x)
     order = _order(sorted_index, sorted_value)
