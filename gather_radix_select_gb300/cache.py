@@ -207,8 +207,8 @@ def cache_attention(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tens
         if listed != rows:
             raise ValueError("idx must have one row per row of q")
         idx_type = _IDX[idx.dtype]
-        # an empty list has no address of its own: any address says that idx was given
-        idx_ptr = idx.data_ptr() if n > 0 else page_table.data_ptr() or q.data_ptr()
+        # an empty list has no address of its own: any says that idx was given, and that of q has the alignment
+        idx_ptr = idx.data_ptr() if n > 0 else q.data_ptr()
     if out is not None and (out.shape != (rows, h, dv) or not out.is_contiguous() or out.dtype != torch.bfloat16
                             or out.device != dev):
         raise ValueError("out must be a contiguous bf16 [rows, h, dv] tensor")
