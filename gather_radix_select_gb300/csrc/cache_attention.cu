@@ -60,6 +60,7 @@ constexpr int kMaxCols = 128;              // (row, head) columns of a CTA at mo
 constexpr int kMaxRing = 5;
 constexpr int kValidSlots = 16;            // tiles whose validity bits are kept (more than the ring holds)
 constexpr int kNoted = 8;                  // tiles whose validity bits may be under way (the ring holds 5, lookups are 2 ahead)
+constexpr int kScan = 32768;               // entries of a list's end that are looked through for its last position
 constexpr int kUnits = 4;                  // units known at a time
 constexpr int kMaxItems = 512;             // items whose tiles are shared out evenly at most
 constexpr int kMaxCtas = 512;              // CTAs that share at most
@@ -397,14 +398,16 @@ __device__ __forceinline__ void make_unit(const Kargs &k, const Misc *m, int u, 
     most = __reduce_max_sync(0xffffffffu, most);
     int64_t keys = most;
     if (k.a.idx) {  // one row: its list up to the last entry that counts
+        // (from the back: the last entries of most lists count.  kScan entries at most: the other roles wait for
+        // the unit meanwhile, and empty tiles before that are no fault.)
         int last = 0;
-        // (from the back: the last entries of most lists count)
+        const int stop = max(k.a.n - kScan, 0);
         auto counts = [&](int64_t p) {
             if (p >= cap && k.a.err_flag) atomicCAS(k.a.err_flag, 0, kCacheInval);
             return p >= 0 && p < most;
         };
 #pragma unroll 1
-        for (int hi = k.a.n; hi > 0 && !__any_sync(0xffffffffu, last > 0); hi -= 128) {
+        for (int hi = k.a.n; hi > stop && !__any_sync(0xffffffffu, last > 0); hi -= 128) {
             int64_t p[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -416,6 +419,7 @@ __device__ __forceinline__ void make_unit(const Kargs &k, const Misc *m, int u, 
                 if (counts(p[i])) last = hi - 128 + i * 32 + lane + 1;
         }
         keys = __reduce_max_sync(0xffffffffu, last);
+        if (keys == 0) keys = stop;
     }
     if (lane == 0) {
         const int64_t tiles = (keys + M - 1) / M;
