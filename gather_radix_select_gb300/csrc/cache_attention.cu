@@ -549,9 +549,9 @@ struct Loader {
         int64_t row, scale;  // element offsets of the lane's position; row -1: none
     };
     struct Place {
-        int page, in_page;  // kNone: no position
+        int page, in_page;  // in_page kNone: no position
     };
-    static constexpr int kNone = -0x7fffffff - 1;
+    static constexpr int kNone = -1;
 
     // The lane's row of a tile in three steps, taken a tile apart so that nothing waits for their loads:
     // the position (of tile i of the unit; -1: none), its page, its row.
@@ -563,10 +563,10 @@ struct Loader {
     }
     __device__ __forceinline__ Place page_of(int64_t pos) const
     {
-        if (pos < 0) return Place{kNone, 0};
+        if (pos < 0) return Place{0, kNone};
         if (pos >= w->list_end) {
             if (k.a.err_flag && pos >= k.a.t.max_pages * k.a.c.page_size) atomicCAS(k.a.err_flag, 0, kCacheInval);
-            return Place{kNone, 0};
+            return Place{0, kNone};
         }
         // (positions are below 2^31, and so is the size of a page where there is a page table)
         const uint32_t p = static_cast<uint32_t>(pos), ps = static_cast<uint32_t>(k.a.c.page_size), col = p / ps;
@@ -574,7 +574,7 @@ struct Loader {
     }
     __device__ __forceinline__ Rows row_of(Place at) const
     {
-        if (at.page == kNone) return Rows{-1, 0};
+        if (at.in_page == kNone) return Rows{-1, 0};
         if (at.page < 0 || at.page >= k.a.c.pages) {
             if (k.a.err_flag) atomicCAS(k.a.err_flag, 0, kCacheInval);
             return Rows{-1, 0};
