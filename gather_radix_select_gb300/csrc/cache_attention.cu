@@ -317,9 +317,9 @@ __device__ __forceinline__ int item_number(const Kargs &k, const Misc *m, int u)
 template <int M>
 __device__ __forceinline__ void find_units(const Kargs &k, Misc *m, int t, int threads)
 {
-    const int items = static_cast<int>(k.p.items), cta = static_cast<int>(blockIdx.x);
+    const int items = static_cast<int>(k.p.items);
     if (!k.p.split) {
-        if (t == 0) m->units = (items - cta + k.p.ctas - 1) / k.p.ctas;
+        if (t == 0) m->units = units_of(items, static_cast<int>(blockIdx.x), k.p.ctas);
         return;
     }
     if (items == 1) {  // (counted with the unit: 1.2 us sooner)

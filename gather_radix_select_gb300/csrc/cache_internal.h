@@ -67,6 +67,14 @@ struct CacheAttnArgs {
     void *ws;
 };
 
+// Of `items` items dealt out in turn to `ctas` CTAs (no more than items), those of one CTA; up to 2^31 - 1 items.
+constexpr int units_of(int items, int cta, int ctas)
+{
+    return static_cast<int>(static_cast<uint32_t>(items - 1 - cta) / static_cast<uint32_t>(ctas)) + 1;
+}
+static_assert(units_of(1, 0, 1) == 1 && units_of(305, 0, 152) == 3 && units_of(305, 1, 152) == 2, "");
+static_assert(units_of(0x7fffffff, 0, 152) == 14128182 && units_of(0x7fffffff, 151, 152) == 14128181, "");
+
 cudaError_t launch_cache_write(const CacheWriteArgs &a, cudaStream_t s);
 cudaError_t launch_cache_gather(const CacheGatherArgs &a, cudaStream_t s);
 cudaError_t launch_cache_attention(const CacheAttnArgs &a, cudaStream_t s);
