@@ -167,7 +167,8 @@ int sel_cache_attention(const void *q, int64_t rows, int64_t h, int64_t q_row_st
     if (st != SEL_OK) return st;
     st = check_table(cache, page_table, b, max_pages, table_stride, rows);
     if (st != SEL_OK) return st;
-    if (h < 1 || dv < 1 || dv > cache->d || !std::isfinite(scale)) return SEL_EINVAL;
+    if (h < 1 || dv < 1 || dv > cache->d || !std::isfinite(scale) || !std::isfinite(scale * kLog2e))
+        return SEL_EINVAL;
     if (idx) {
         if (idx_dtype != SEL_I32 && idx_dtype != SEL_I64) return SEL_EINVAL;
         if (n < 0 || (rows > 1 && idx_row_stride < n)) return SEL_EINVAL;

@@ -92,6 +92,7 @@ SEL_API int sel_cache_gather(const sel_cache *cache, const int32_t *page_table, 
  *   end      int32 [rows] exclusive ends, clamped to [0, max_pages *
  *            page_size]; NULL means that limit for every row.
  *   dv       1 <= dv <= d, a multiple of 8.
+ *   scale    finite, of any sign, at most 2e38 in magnitude.
  *   out      bf16 [rows, h, dv] contiguous, on 16 bytes.
  *   lse      fp32 [rows, h] contiguous, or NULL (natural logarithm).
  *   workspace  device scratch of at least sel_cache_attention_workspace_size
