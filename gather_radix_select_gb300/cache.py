@@ -180,7 +180,8 @@ def cache_attention(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tens
     page table), or, with ``idx`` (int32/int64 [rows, n], a selection's output), to the positions listed there
     (negative: none; at or past ``end``: left out).  Scores are ``scale * <q, row>`` (default 1 / sqrt(d)); the
     value is the row's first ``dv`` elements (default d, at most 512, a multiple of 8).  A row without positions
-    gives zeros and a log-sum of -inf.  Positions a row does not attend to never influence it.
+    gives zeros and a log-sum of -inf.  Positions a row does not attend to never influence it.  Should a wait inside
+    the kernel run out (about 2 s), ``err_flag`` gets SEL_ETIMEOUT and the rows lost by it are NaN.
 
     Returns ``(out, lse)``: bf16 [rows, h, dv], and fp32 [rows, h] (natural log of the sum of exponentials) with
     ``return_lse``, else None.

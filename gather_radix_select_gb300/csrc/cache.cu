@@ -41,10 +41,11 @@ __device__ __forceinline__ void load8(const void *x, bool bf16, int64_t at, floa
 __device__ __forceinline__ uint32_t quotient(uint32_t a, uint32_t b, int shift) { return shift >= 0 ? a >> shift : a / b; }
 
 // One run of 128 elements of one token by 16 lanes.  The elements are on their way while the slot is read.
-// Instructions bound it (61% of the issue slots, 20% of the DRAM bandwidth), so divisions by powers of two are
-// shifts and the magnitudes a floating-point maximum: 16384 rows of 512 to 8 bits take 10.3 us for 25 MB,
-// 100001 rows of 128 fp32 to bf16 12.6 us for 77 MB (6.1 TB/s).  32 rows, in 4.2 us, are a launch and two
-// loads one after the other.
+// To 8 bits no unit is near its limit (42% of the issue slots over the kernel's time, 20% of the DRAM bandwidth):
+// each of the many short CTAs is a chain of loads, shuffles and conversions.  Divisions by powers of two are
+// shifts and the magnitudes a floating-point maximum.  16384 rows of 512 to 8 bits take 10.2 us a call for 25 MB,
+// 6.8 us one after the other in a graph; 100001 rows of 128 fp32 to bf16 14.4 us and 8.2 us for 77 MB.  32 rows,
+// 1.8 us in a graph, are two loads one after the other.
 __global__ void __launch_bounds__(kWriteThreads) cache_write_kernel(const CacheWriteArgs a, uint32_t runs, int runs_shift,
                                                                     int page_shift, uint32_t items)
 {

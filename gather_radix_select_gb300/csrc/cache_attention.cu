@@ -14,7 +14,7 @@
 // the columns' maxima are formed across the positions and the sums and accumulators are rescaled.  Scores, sums,
 // references and accumulators are fp32; the weights are rounded to bf16 for the second product, whose other
 // operand, the value, has no more bits (the sums are of the unrounded weights: the roundings are to
-// nearest, 2^-9 of a weight at most).  Sums are kept per thread (its positions) and joined at the end in a fixed order.
+// nearest, 2^-8 of a weight at most).  Sums are kept per thread (its positions) and joined at the end in a fixed order.
 //
 // A CTA stays on its SM and takes one unit of work (rows x heads x a part of the positions) after the
 // other.  Its warps are those of the softmax in groups of 4, one that issues the products, one that looks up
@@ -26,23 +26,26 @@
 // row's parts come to, sums and accumulators, a second kernel joins in a fixed order.
 //
 // What bounds it.  Of 512 elements one tile fills the ring beside the queries, so a tile's steps follow one
-// another: values, the next rows' way in, scores, softmax, 7300 cycles in all, of which the products'
-// 64 instructions take 3100 at their own rate.  Of 128 .. 192 elements the softmax bounds: 2200 of 2800 cycles
-// a tile, against 1800 of products.  8-bit rows: decoding them, 3000 cycles a chunk and set of warps, loads
-// included.  And one-off code: what runs once a unit is fetched from far, about 100 cycles for 8 instructions,
+// another: values, the next rows' way in, scores, softmax, 7100 cycles in all (3.4 us at the 2070 MHz of all
+// figures here, 108 tiles of the busiest CTA in the 371 us below), of which the products' 64 instructions take
+// 3100 at their own rate.  8-bit rows: 10000 cycles a tile (4.8 us, 28 tiles in the 135 us below): each of the two
+// sets of warps loads and decodes two chunks one after the other, and the second one's loads start when the
+// products have freed its place.  Of 128 .. 192 elements the softmax bounds, against 1800 cycles of products a tile:
+// 3700 cycles a tile with the units' starts and ends (103 tiles, 189 us).  And one-off code: what runs once a unit is fetched from far, about 100 cycles for 8 instructions,
 // so masks, column maxima and sums are written for few instructions (the last tile's mask took 6300 cycles
 // before, the sums 5400).
 // Measured (GB300, device time; of the 1891 TFLOP/s and 6772 GB/s that plain products and copies reach):
-//   4096 rows x 64 heads over 512 selected rows of 512, bf16   364 us   660 TFLOP/s (35%)
-//   4 rows x 64 heads over 204800 positions of 512, bf16       170 us   4930 GB/s (73%)
-//   3 x 701 rows x 24 heads, 5000 positions of 192, causal     184 us   708 TFLOP/s (37%)
-//   1024 rows x 64 heads over 512 selected 8-bit rows of 512   136 us   504 TFLOP/s (27%)
-//   32 rows x 64 heads over <= 16384 positions of 512, 8 bits  120 us   1830 GB/s, 446 TFLOP/s (27%)
-//   1 row over 1000 positions of 128                           12.6 us  (latency: start, lookups, a tile, join)
+//   4096 rows x 64 heads over 512 selected rows of 512, bf16   371 us   649 TFLOP/s (34%)
+//   4 rows x 64 heads over 204800 positions of 512, bf16       169 us   4940 GB/s (73%)
+//   3 x 701 rows x 24 heads, 5000 positions of 192, causal     189 us   689 TFLOP/s (36%)
+//   1024 rows x 64 heads over 512 selected 8-bit rows of 512   135 us   507 TFLOP/s (27%)
+//   32 rows x 64 heads over <= 16384 positions of 512, 8 bits  119 us   1840 GB/s, 448 TFLOP/s (27%)
+//   1 row over 1000 positions of 128                           10.9 us  (in a graph; latency: start, lookups, a tile, join)
 // Tried and slower: tiles of 64 positions (45 cycles an instruction of half the work); pairs of CTAs that share
 // a row (622 us against 385 then); TMA gathers of 4 rows (75 to 108 cycles for 512 bytes); bf16 rows through
 // registers (564 us); the next tile's rows prefetched into L2 (415 us: the copies fill the path already);
 // scores and values issued by a warp each (no change); a warp that looks up the rows for the others (448 us).
+// (A few per cent either way say little about an idea here: the order of the roles' code alone moves as much.)
 #include <atomic>
 #include <cstddef>
 #include <cstdint>

@@ -99,6 +99,10 @@ SEL_API int sel_cache_gather(const sel_cache *cache, const int32_t *page_table, 
  *            bytes, 256-byte aligned, any contents; may be NULL when that is 0.
  * A row without positions gives zeros and lse = -inf.  Positions that a row
  * does not attend to have no influence on it, whatever their cache rows hold.
+ * An infinity past the first dv elements counts by its score alone (a score of
+ * -inf has the weight 0).  A row that attends to a cache row with an infinity
+ * or NaN among the first dv elements gets results that are not finite; whether
+ * only the elements that the formula makes so, or all and lse, is not specified.
  * Positions past the page table, or whose page is not in [0, pages), are left
  * out and set *err_flag = SEL_EINVAL.  Sums and the softmax are in fp32; the
  * weights are rounded to bf16 for the product with the values.
