@@ -69,8 +69,8 @@ constexpr int kMaxItems = 512;             // items whose tiles are shared out e
 constexpr int kMaxCtas = 512;              // CTAs that share at most
 constexpr int kStart = 1;                  // tiles that an item's start counts for there
 // A column's reference is set 2^kHeadroom above its largest weight so far and moves when a weight reaches
-// twice the reference.  bf16 has the range of fp32, so the small weights lose nothing by it, and that
-// a weight is 2 or more is one bit of its bf16 exponent.
+// twice the reference.  bf16 has the range of fp32, so the small weights lose nothing by it down to 2^-102 of the
+// column's largest (below, they are 0), and that a weight is 2 or more is one bit of its bf16 exponent.
 constexpr float kHeadroom = 24.0f;
 constexpr float kNoReference = -3.4028235e38f;  // of a column without a score above -inf: any such score outgrows it
 constexpr long long kWaitCycles = 4000000000LL;  // about 2 s: no wait of a working kernel takes a thousandth of it
