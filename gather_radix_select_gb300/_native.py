@@ -34,7 +34,13 @@ class SelCache(ctypes.Structure):
                 ("scale_row_stride", _i64)]
 
 
-_cache_p = ctypes.POINTER(SelCache)
+class SelRotation(ctypes.Structure):
+    """sel_rotation of include/sel/cache_serving.h."""
+    _fields_ = [("table", _vp), ("positions", _i64), ("stride", _i64), ("first", _i64), ("rot", _i64),
+                ("interleaved", _int)]
+
+
+_cache_p, _rotation_p = ctypes.POINTER(SelCache), ctypes.POINTER(SelRotation)
 SIGNATURES = {
     "sel_stride_requirement": (_int, [ctypes.POINTER(_int), ctypes.POINTER(_int)]),
     "sel_topk": (_int, [_vp, _int, _i64, _i64, _i64, _vp, _int, _int, _int, _int,
@@ -65,6 +71,14 @@ SIGNATURES = {
     "sel_cache_attention": (_int, [_vp, _i64, _i64, _i64, _i64, _cache_p, _vp, _i64, _i64, _i64, _vp, _vp, _int,
                                    _i64, _i64, _i64, ctypes.c_float, _vp, _vp, _vp, ctypes.c_size_t, _vp, _vp]),
     "sel_cache_set_wait_limit": (_int, [_i64]),
+    "sel_cache_append": (_int, [_vp, _int, _i64, _i64, _cache_p, _vp, _i64, _i64, _i64, _vp, _int, _rotation_p, _vp,
+                                _int, _i64, _i64, _i64, _vp, _vp, _vp]),
+    "sel_cache_attention_window": (_int, [_vp, _i64, _i64, _i64, _i64, _cache_p, _vp, _i64, _i64, _i64, _vp, _i64,
+                                          _i64, _i64, ctypes.c_float, _vp, _vp, _vp, ctypes.c_size_t, _vp, _vp]),
+    "sel_cache_attention_window_workspace_size": (ctypes.c_size_t, [_i64] * 9),
+    "sel_cache_attention_shared": (_int, [_vp, _i64, _i64, _i64, _i64, _cache_p, _vp, _i64, _i64, _i64, _vp, _i64,
+                                          _i64, ctypes.c_float, _vp, _vp, _vp, ctypes.c_size_t, _vp, _vp]),
+    "sel_cache_attention_shared_workspace_size": (ctypes.c_size_t, [_i64] * 8),
     "sel_cache_attention_workspace_size": (ctypes.c_size_t, [_i64, _i64, _i64, _i64, _i64, _i64, _i64, _int, _i64]),
 }
 

@@ -1,5 +1,5 @@
 // cache_internal.h -- argument blocks and launchers of the paged-cache operators, shared by the
-// C-ABI layer (cache_api.cu) and the kernels (cache.cu, cache_attention.cu).
+// C-ABI layer (cache_api.cu) and the kernels (cache*.cu).
 #pragma once
 
 #include <cstddef>
@@ -49,6 +49,30 @@ struct CacheGatherArgs {
     int32_t pairs;  // positions of a CTA, set by the launcher
 };
 
+// What a row attends to of the positions below its end, where no list says it; 32 bits: so are positions.
+struct Seen {
+    int32_t window;  // the last `window` of them and those below `sinks`; 0: all
+    int32_t sinks;
+    int32_t shared;  // positions below this are the same rows for all sequences; 0: none
+};
+
+struct CacheAppendArgs {
+    CacheRef c;
+    PageTable t;
+    const void *x;
+    int64_t tokens, x_stride;
+    const void *positions;
+    const float *rotation;  // [rot_rows, rot_stride]: rot / 2 cosines, rot / 2 sines
+    int64_t rot_rows, rot_stride;
+    int32_t first, rot;     // the rotated run of a row
+    int32_t interleaved;    // pairs are neighbours, else rot / 2 apart
+    int32_t pos_i64, x_bf16, q_bf16;
+    const void *q;          // nullable
+    int64_t h, q_row_stride, q_head_stride;
+    uint16_t *q_out;
+    int32_t *err_flag;
+};
+
 struct CacheAttnArgs {
     CacheRef c;
     PageTable t;
@@ -65,6 +89,7 @@ struct CacheAttnArgs {
     float *lse;          // nullable
     int32_t *err_flag;   // nullable
     void *ws;
+    Seen seen;           // without a list only
 };
 
 // Of `items` items dealt out in turn to `ctas` CTAs (no more than items), those of one CTA; up to 2^31 - 1 items.
@@ -77,6 +102,7 @@ static_assert(units_of(0x7fffffff, 0, 152) == 14128182 && units_of(0x7fffffff, 1
 
 cudaError_t launch_cache_write(const CacheWriteArgs &a, cudaStream_t s);
 cudaError_t launch_cache_gather(const CacheGatherArgs &a, cudaStream_t s);
+cudaError_t launch_cache_append(const CacheAppendArgs &a, cudaStream_t s);
 cudaError_t launch_cache_attention(const CacheAttnArgs &a, cudaStream_t s);
 
 // Cycles after which a wait of the attention kernel gives up, from the next call on; negative: the usual ones.
@@ -84,7 +110,7 @@ void set_cache_wait_cycles(long long cycles);
 
 // Workspace bytes of an attention call; launches nothing.
 size_t cache_attention_workspace(int64_t rows, int64_t h, int64_t d, int64_t dv, int64_t b, int64_t positions,
-                                 bool idx_given);
+                                 bool idx_given, const Seen &seen);
 
 #ifdef __CUDACC__
 // Flat row offset (page * page_size + place) does not serve strided pages, so rows are found by page
