@@ -1,4 +1,5 @@
-"""ctypes binding of libsel.so (include/sel.h).  Argument marshalling only.
+"""ctypes binding of libsel.so (include/sel.h, include/sel/*.h).  Argument marshalling only.  (The calls of
+include/sel/cache_serving.h go by a compiled module, ``binding()``: csrc/binding.cpp says why.)
 
 The library is built in-tree by ``gather_radix_select_gb300.build``; loading
 fails loudly (``RuntimeError``) when it is missing -- there is no fallback.
@@ -6,6 +7,8 @@ fails loudly (``RuntimeError``) when it is missing -- there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import threading
 
@@ -113,6 +116,27 @@ def load(build_if_missing: bool = False):
             fn.argtypes = args
         _lib = lib
         return lib
+
+
+_binding = None
+
+
+def binding():
+    """The module of csrc/binding.cpp, bound to the loaded library.  Raises RuntimeError when it is not built."""
+    global _binding
+    if _binding is not None:
+        return _binding
+    lib = load()
+    with _lock:
+        if _binding is None:
+            path = _build.binding_path()
+            if not os.path.exists(path):
+                raise RuntimeError("%s is not built; run `python -m gather_radix_select_gb300.build`" % path)
+            loader = importlib.machinery.ExtensionFileLoader("_binding", path)
+            module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_binding", loader))
+            module.bind(lib._handle)
+            _binding = module
+        return _binding
 
 
 class SelError(RuntimeError):

@@ -1,4 +1,4 @@
-"""Builds libsel.so (the CUDA kernels + C ABI) in-tree for sm_103a.
+"""Builds libsel.so (the CUDA kernels + C ABI) in-tree for sm_103a, and the Python module that calls its serving part.
 
     python -m gather_radix_select_gb300.build [--force] [--debug] [-v]
 
@@ -11,6 +11,9 @@ defined, whose kernels check selected accesses (staged-list and region
 offsets, workspace slots, output positions, gathered key rows), skip the ones
 that would leave their buffer and report SEL_EBOUNDS in err_flag.  It is
 loaded instead of libsel.so when SEL_LIBRARY=debug is set.
+
+csrc/binding.cpp, the module _binding, is compiled by g++ against the installed PyTorch, whose version its file's name
+has (its ABI goes with the version).
 """
 from __future__ import annotations
 
@@ -19,6 +22,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -88,11 +92,43 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
     return so
 
 
+def binding_path() -> str:
+    import torch
+    return os.path.join(OUT_DIR, "binding-%s" % torch.__version__, "_binding.so")
+
+
+def build_binding(force: bool = False, verbose: bool = False) -> str:
+    """The Python module of csrc/binding.cpp."""
+    import torch
+    so = binding_path()
+    if not force and up_to_date(so):
+        return so
+    os.makedirs(os.path.dirname(so), exist_ok=True)
+    home, cuda = os.path.dirname(torch.__file__), os.path.dirname(os.path.dirname(nvcc()))
+    libs = os.path.join(home, "lib")
+    tmp = so + ".tmp%d" % os.getpid()
+    cmd = [os.environ.get("CXX") or shutil.which("g++") or "c++", "-O2", "-std=c++17", "-shared", "-fPIC",
+           "-fvisibility=hidden", "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI,
+           os.path.join(CSRC, "binding.cpp"), "-o", tmp, "-isystem", os.path.join(home, "include"), "-isystem",
+           os.path.join(home, "include", "torch", "csrc", "api", "include"), "-isystem", os.path.join(cuda, "include"),
+           "-isystem", sysconfig.get_paths()["include"], "-L" + libs, "-Wl,-rpath," + libs, "-ltorch_python", "-ltorch",
+           "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if verbose or r.returncode != 0:
+        sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed for binding.cpp")
+    os.replace(tmp, so)
+    return so
+
+
 def build_all(force: bool = False) -> list[str]:
-    """libsel.so and libsel_debug.so, compiled side by side."""
-    with concurrent.futures.ThreadPoolExecutor(max_workers=2) as ex:
-        return list(ex.map(lambda d: build(force=force, debug=d), (False, True)))
+    """libsel.so, libsel_debug.so and the binding, compiled side by side."""
+    with concurrent.futures.ThreadPoolExecutor(max_workers=3) as ex:
+        jobs = [ex.submit(build, force=force), ex.submit(build, force=force, debug=True), ex.submit(build_binding, force)]
+        return [j.result() for j in jobs]
 
 
 if __name__ == "__main__":
     print(build(force="--force" in sys.argv, verbose="-v" in sys.argv, debug="--debug" in sys.argv))
+    print(build_binding(force="--force" in sys.argv, verbose="-v" in sys.argv))

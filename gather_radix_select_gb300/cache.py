@@ -1,8 +1,8 @@
 """Paged key cache: rows written (quantised) at their slots or appended at their positions, read back, attended to.
 
-Python face of ``include/sel/cache.h`` and ``include/sel/cache_serving.h``, in the manner of the package's top-k and gather: PyTorch supplies
-device memory and the stream, every step of the computation runs in the library's kernels, argument errors
-raise before a launch, findings made on the device go to a caller-zeroed ``err_flag``.
+Python face of ``include/sel/cache.h`` and ``include/sel/cache_serving.h``, in the manner of the package's top-k
+and gather: PyTorch supplies device memory and the stream, every step of the computation runs in the library's
+kernels, argument errors raise before a launch, findings made on the device go to a caller-zeroed ``err_flag``.
 
 A cache is ``[pages, page_size, d]``: bf16 rows, or ``torch.float8_e4m3fn`` codes with ``scales`` fp32
 ``[pages, page_size, ceil(d / 128)]`` (value = code * scale; ``cache_write`` stores powers of two).  One row a
@@ -105,14 +105,10 @@ def _launch(dev, stream, call):
 
 
 @functools.lru_cache(maxsize=4096)
-def _scratch_bytes(device_index, rows, h, d, dv, b, max_pages, page_size, idx_given, n, window, sinks, shared):
+def _scratch_bytes(device_index, rows, h, d, dv, b, max_pages, page_size, idx_given, n):
     """Scratch that a call of this shape needs on the (current) device."""
-    lib = _native.load()
-    if window is not None:
-        return int(lib.sel_cache_attention_window_workspace_size(rows, h, d, dv, b, max_pages, page_size, window, sinks))
-    if shared:
-        return int(lib.sel_cache_attention_shared_workspace_size(rows, h, d, dv, b, max_pages, page_size, shared))
-    return int(lib.sel_cache_attention_workspace_size(rows, h, d, dv, b, max_pages, page_size, idx_given, n))
+    return int(_native.load().sel_cache_attention_workspace_size(rows, h, d, dv, b, max_pages, page_size, idx_given,
+                                                                 n))
 
 
 def cache_write(x: torch.Tensor, cache: torch.Tensor, slots: torch.Tensor, *, scales: torch.Tensor | None = None,
@@ -162,55 +158,15 @@ def cache_append(x: torch.Tensor, cache: torch.Tensor, page_table: torch.Tensor,
     padding token are returned as they are.  Without, None is returned.  A position past the page table or the
     rotation's table, or on a page outside the cache, writes nothing and sets ``err_flag``.
     """
-    c = _cache_struct(cache, scales)
-    dev = cache.device
-    x_type = _ROWS.get(x.dtype)
-    if x_type is None or x.dim() != 2 or x.device != dev or x.shape[1] != c.d:
-        raise ValueError("x must be a bfloat16 or float32 tensor [tokens, d] on the cache's device")
-    tokens, d = x.shape
-    x_stride, one = x.stride()
-    if one != 1 and d > 1:
-        raise ValueError("rows of x must be contiguous")
-    b, m, table_stride = _table(page_table, dev)
-    pos_type = _IDX.get(positions.dtype)
-    if pos_type is None or positions.dim() != 1 or positions.shape[0] != tokens or positions.device != dev \
-            or not positions.is_contiguous():
-        raise ValueError("positions must be a contiguous int32/int64 tensor with one entry per token")
-    if rotation.dtype != torch.float32 or rotation.dim() != 2 or rotation.device != dev:
-        raise ValueError("rotation must be a float32 tensor [positions, rot] on the cache's device")
-    known, rot = rotation.shape
-    rot_stride, one = rotation.stride()
-    if one != 1 and rot > 1:
-        raise ValueError("rows of rotation must be contiguous")
-    turn = _native.SelRotation(rotation.data_ptr(), known, rot_stride if known > 1 else rot,
-                               d - rot if first is None else int(first), rot, bool(interleaved))
-    h = q_row = q_head = q_type = 0
-    q_ptr = None
-    if q is not None:
-        q_type = _ROWS.get(q.dtype)
-        if q_type is None or q.dim() != 3 or q.device != dev or q.shape[0] != tokens or q.shape[2] != d:
-            raise ValueError("q must be a bfloat16 or float32 tensor [tokens, h, d] on the cache's device")
-        h = q.shape[1]
-        q_row, q_head, one = q.stride()
-        if one != 1 and d > 1:
-            raise ValueError("q must be contiguous in its last dimension")
-        q_row, q_head = q_row if tokens > 1 else h * d, q_head if h > 1 else d
-        q_ptr = q.data_ptr() if tokens > 0 else x.data_ptr()
-    if q_out is not None and (q is None or q_out.shape != q.shape or not q_out.is_contiguous()
-                              or q_out.dtype != torch.bfloat16 or q_out.device != dev):
-        raise ValueError("q_out must be a contiguous bf16 tensor of q's shape")
-    err = _flag(err_flag, dev)
-
-    def call(s):
-        to = torch.empty((tokens, h, d), dtype=torch.bfloat16, device=dev) if q is not None and q_out is None else q_out
-        return _native.load().sel_cache_append(
-            x.data_ptr(), x_type, tokens, x_stride if tokens > 1 else d, c, page_table.data_ptr(), b, m, table_stride,
-            positions.data_ptr(), pos_type, turn, q_ptr, q_type, h, q_row, q_head,
-            None if to is None else to.data_ptr(), err, s), to
-
-    st, to = _launch(dev, stream, call)
-    _native.check(st, "sel_cache_append")
-    return to
+    args = (x, cache, page_table, positions, rotation, scales, first, interleaved, q, q_out, err_flag)
+    if stream is None:
+        got = _native.binding().cache_append(*args)
+    else:
+        with torch.cuda.device(cache.device), torch.cuda.stream(stream):
+            got = _native.binding().cache_append(*args)
+    if got.__class__ is int:
+        _native.check(got, "sel_cache_append")
+    return got
 
 
 def cache_gather(cache: torch.Tensor, page_table: torch.Tensor, idx: torch.Tensor, *,
@@ -266,6 +222,22 @@ def cache_attention(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tens
     Returns ``(out, lse)``: bf16 [rows, h, dv], and fp32 [rows, h] (natural log of the sum of exponentials) with
     ``return_lse``, else None.
     """
+    if window is not None or shared or sinks:
+        if idx is not None or (window is not None and shared):
+            raise ValueError("at most one of idx, window and shared")
+        if window is None and sinks:
+            raise ValueError("sinks are the positions that stay visible outside a window")
+        if shared < 0 or sinks < 0 or (window is not None and window < 1):
+            raise ValueError("window must be at least 1, sinks and shared not negative")
+        args = (q, cache, page_table, scales, end, dv, scale, return_lse, out, err_flag, window, sinks, shared)
+        if stream is None:
+            got = _native.binding().cache_attention(*args)
+        else:
+            with torch.cuda.device(cache.device), torch.cuda.stream(stream):
+                got = _native.binding().cache_attention(*args)
+        if got.__class__ is int:
+            _native.check(got, "sel_cache_attention_window" if window is not None else "sel_cache_attention_shared")
+        return got
     c = _cache_struct(cache, scales)
     dev = cache.device
     b, m, table_stride = _table(page_table, dev)
@@ -281,15 +253,6 @@ def cache_attention(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tens
         raise ValueError("end must be a contiguous int32 tensor with one entry per row")
     dv = d if dv is None else int(dv)
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
-    if (idx is not None) + (window is not None) + (shared != 0) > 1:
-        raise ValueError("at most one of idx, window and shared")
-    if window is None:
-        if sinks != 0:
-            raise ValueError("sinks are the positions that stay visible outside a window")
-    elif window < 1 or sinks < 0:
-        raise ValueError("window must be at least 1 and sinks not negative")
-    if shared < 0:
-        raise ValueError("shared must not be negative")
     n = idx_stride = idx_type = 0
     idx_ptr = None
     if idx is not None:
@@ -308,19 +271,15 @@ def cache_attention(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tens
         lib = _native.load()
         to = torch.empty((rows, h, max(dv, 0)), dtype=torch.bfloat16, device=dev) if out is None else out
         lse = torch.empty((rows, h), dtype=torch.float32, device=dev) if return_lse else None
-        need = _scratch_bytes(dev.index, rows, h, d, dv, b, m, c.page_size, idx_ptr is not None, n, window, sinks, shared)
+        need = _scratch_bytes(dev.index, rows, h, d, dv, b, m, c.page_size, idx_ptr is not None, n)
         # Scratch of the call's own, from the stream's pool: two launches pass data through it, and another thread's
         # call on the same stream may come between them.
         ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-        rest = (dv, scale, to.data_ptr(), None if lse is None else lse.data_ptr(), None if ws is None else ws.data_ptr(),
-                need, err, s)
-        q_args = (q.data_ptr(), rows, h, q_row if rows > 1 else h * d, q_head if h > 1 else d, c, page_table.data_ptr(),
-                  b, m, table_stride, None if end is None else end.data_ptr())
-        if window is not None:
-            return lib.sel_cache_attention_window(*q_args, window, sinks, *rest), to, lse
-        if shared:
-            return lib.sel_cache_attention_shared(*q_args, shared, *rest), to, lse
-        return lib.sel_cache_attention(*q_args, idx_ptr, idx_type, n, idx_stride, *rest), to, lse
+        return lib.sel_cache_attention(
+            q.data_ptr(), rows, h, q_row if rows > 1 else h * d, q_head if h > 1 else d, c, page_table.data_ptr(),
+            b, m, table_stride, None if end is None else end.data_ptr(), idx_ptr, idx_type, n, idx_stride, dv,
+            scale, to.data_ptr(), None if lse is None else lse.data_ptr(), None if ws is None else ws.data_ptr(),
+            need, err, s), to, lse
 
     st, to, lse = _launch(dev, stream, call)
     _native.check(st, "sel_cache_attention")
