@@ -103,7 +103,7 @@ int sm_count()
     return n;
 }
 
-Plan plan_of(int64_t rows, int64_t h, int64_t d, int64_t b, int64_t positions, bool idx_given)
+Plan plan_of(int64_t rows, int64_t h, int64_t d, int64_t b, int64_t positions, bool idx_given, int64_t sms)
 {
     Plan p{};
     const int64_t per = rows / b;
@@ -120,7 +120,6 @@ Plan plan_of(int64_t rows, int64_t h, int64_t d, int64_t b, int64_t positions, b
     // Few items: their tiles are shared out, where that leaves the fewest tiles in a row, counting a part's start
     // and end as 1.5 tiles and the join as 1.
     const int64_t tiles = positions > 128 ? (positions + 127) / 128 : 1;
-    const int64_t sms = sm_count() > 0 ? sm_count() : 1;
     const int64_t waves = (p.items + sms - 1) / sms;
     const double whole = static_cast<double>(waves) * (static_cast<double>(tiles) + 1.5);
     const int64_t all = p.items * (tiles + kStart), most = sms < kMaxCtas ? sms : kMaxCtas, ctas = all < most ? all : most;
@@ -133,14 +132,13 @@ Plan plan_of(int64_t rows, int64_t h, int64_t d, int64_t b, int64_t positions, b
 // The same under a window: `reach` positions at most are visible to a row, and fewer than rows_per_tile more to the rows
 // of a tile where their ends follow one another.  (Where they do not, an item may be as long as the page table, whose
 // tiles have to be countable all the same.)
-Plan plan_window(int64_t rows, int64_t h, int64_t d, int64_t b, int64_t positions, int64_t reach)
+Plan plan_window(int64_t rows, int64_t h, int64_t d, int64_t b, int64_t positions, int64_t reach, int64_t sms)
 {
-    Plan p = plan_of(rows, h, d, b, positions, false);
+    Plan p = plan_of(rows, h, d, b, positions, false, sms);
     const int64_t most = reach + p.rows_per_tile - 1;
     if (most >= positions) return p;
-    p = plan_of(rows, h, d, b, most, false);
-    const int64_t sms = sm_count() > 0 ? sm_count() : 1;
-    if (p.split && p.items * (positions / 128 + 1 + kStart) >= 0x7fffffff / (sms + 1)) {
+    p = plan_of(rows, h, d, b, most, false, sms);
+    if (p.split && p.items * (positions / 128 + 1 + kStartRanges) >= 0x7fffffff / (sms + 1)) {
         p.split = 0;
         p.ctas = static_cast<int>(p.items < sms ? p.items : sms);
     }
@@ -150,9 +148,9 @@ Plan plan_window(int64_t rows, int64_t h, int64_t d, int64_t b, int64_t position
 // With a shared prefix: the rows of all sequences attend to it by tiles of their own, where a sequence's rows do not
 // fill a tile by themselves, and where that makes less of the work, counted as in plan_of (there a part's or an
 // item's start, here the join is always taken).  Else prefix_items is 0, and every sequence reads its own page table.
-Plan plan_shared(int64_t rows, int64_t h, int64_t d, int64_t b, int64_t positions, int64_t shared)
+Plan plan_shared(int64_t rows, int64_t h, int64_t d, int64_t b, int64_t positions, int64_t shared, int64_t sms)
 {
-    const Plan plain = plan_of(rows, h, d, b, positions, false);
+    const Plan plain = plan_of(rows, h, d, b, positions, false, sms);
     const int64_t per = rows / b, prefix = shared < positions ? shared : positions;
     const int64_t cols = d <= 192 && h * rows > 64 ? 128 : 64;
     if (prefix <= 0 || b < 2 || h * per >= cols) return plain;
@@ -165,12 +163,13 @@ Plan plan_shared(int64_t rows, int64_t h, int64_t d, int64_t b, int64_t position
     p.prefix_rows = static_cast<int>(cols / h < rows ? cols / h : rows);
     p.prefix_items = (rows + p.prefix_rows - 1) / p.prefix_rows;
     p.items = p.prefix_items + b;
-    const int64_t sms = sm_count() > 0 ? sm_count() : 1, most = sms < kMaxCtas ? sms : kMaxCtas;
+    const int64_t most = sms < kMaxCtas ? sms : kMaxCtas;
     const int64_t own = (positions - prefix + 127) / 128;
-    const int64_t all = p.prefix_items * ((prefix + 127) / 128 + kStart) + b * (own + kStart);
+    const int64_t all = p.prefix_items * ((prefix + 127) / 128 + kStartRanges) + b * (own + kStartRanges);
     p.split = p.items <= kMaxItems && all < 0x7fffffff / (sms + 1);
     p.ctas = static_cast<int>(p.split ? (all < most ? all : most) : p.items < sms ? p.items : sms);
-    const double grouped = static_cast<double>((all + sms - 1) / sms) + 1.5 + 1.0;
+    const int64_t counted = all - p.items * (kStartRanges - kStart);  // (a start counts for both alike)
+    const double grouped = static_cast<double>((counted + sms - 1) / sms) + 1.5 + 1.0;
     const int64_t tiles = (positions + 127) / 128, waves = (plain.items + sms - 1) / sms;
     const double apart = plain.split ? static_cast<double>((plain.items * (tiles + kStart) + plain.ctas - 1) / plain.ctas) + 1.5 + 1.0
                                      : static_cast<double>(waves) * (static_cast<double>(tiles) + 1.5);
@@ -179,9 +178,10 @@ Plan plan_shared(int64_t rows, int64_t h, int64_t d, int64_t b, int64_t position
 
 Plan plan_for(int64_t rows, int64_t h, int64_t d, int64_t b, int64_t positions, bool idx_given, const Seen &seen)
 {
-    if (seen.window > 0) return plan_window(rows, h, d, b, positions, int64_t{seen.window} + seen.sinks);
-    if (seen.shared > 0) return plan_shared(rows, h, d, b, positions, seen.shared);
-    return plan_of(rows, h, d, b, positions, idx_given);
+    const int64_t known = sm_count(), sms = known > 0 ? known : 1;
+    if (seen.window > 0) return plan_window(rows, h, d, b, positions, int64_t{seen.window} + seen.sinks, sms);
+    if (seen.shared > 0) return plan_shared(rows, h, d, b, positions, seen.shared, sms);
+    return plan_of(rows, h, d, b, positions, idx_given, sms);
 }
 
 size_t rounded(size_t n) { return (n + 255) / 256 * 256; }
@@ -233,7 +233,8 @@ cudaError_t launch_cache_attention(const CacheAttnArgs &a, cudaStream_t s)
     int vecs = 32;
     while (vecs * 4 < a.dv) vecs *= 2;
     const int64_t columns = grouped ? a.rows * a.h : k.p.items * k.p.cols;
-    const int64_t parts = (k.p.ctas + k.p.items) / k.p.items, sms = sm_count();
+    // (of a shared prefix's items, which are cut most, as many as all CTAs come to)
+    const int64_t cut = grouped ? k.p.prefix_items : k.p.items, parts = k.p.split ? (k.p.ctas + cut) / cut : 2, sms = sm_count();
     int threads = vecs;
     while (threads < kJoinThreads && threads / vecs * 2 < parts && columns * threads * 2 <= 2048 * sms) threads *= 2;
     cudaLaunchConfig_t at = {};

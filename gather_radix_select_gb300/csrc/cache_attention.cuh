@@ -99,6 +99,9 @@ constexpr int kUnits = 4;                  // units known at a time
 constexpr int kMaxItems = 512;             // items whose tiles are shared out evenly at most
 constexpr int kMaxCtas = 512;              // CTAs that share at most
 constexpr int kStart = 1;                  // tiles that an item's start counts for there
+// With ranges, whose items are often short, what it does take (48 sequences behind 204800 positions of 128: the busiest
+// CTA 63 us with 1, the median 58; 77.9 us in all with 1, 76.8 with 2, 76.4 with 3, 77.4 with 4).
+constexpr int kStartRanges = 3;
 // A column's reference is set 2^kHeadroom above its largest weight so far and moves when a weight reaches
 // twice the reference.  bf16 has the range of fp32, so the small weights lose nothing by it down to 2^-102 of the
 // column's largest (below, they are 0), and that a weight is 2 or more is one bit of its bf16 exponent.
@@ -336,12 +339,15 @@ __device__ __forceinline__ Share share_of(int all, const Kargs &k)
     return cta < ctas ? Share{all * cta / ctas, all * (cta + 1) / ctas, ctas} : Share{all, all, ctas};
 }
 
+template <bool RANGES>
+__device__ __forceinline__ int start_of(const Kargs &k) { return RANGES && k.p.items > 1 ? kStartRanges : kStart; }
+
 // What an item counts for there, of which the last row's positions end at `most`.
-template <int M>
+template <int M, bool RANGES>
 __device__ __forceinline__ int weight_of(const Kargs &k, int most)
 {
     if (k.a.idx && most > 0) most = k.a.n;  // (never with RANGES, whose ends are numbers)
-    return kStart + most / M + (most % M != 0);
+    return start_of<RANGES>(k) + most / M + (most % M != 0);
 }
 
 // Where the sums and accumulators of the CTA's unit u go, an item's [at, after) of all `all` tiles; -1: nowhere, it is
@@ -371,7 +377,7 @@ __device__ __forceinline__ int item_number(const Kargs &k, const Misc *m, int u)
 }
 
 // All threads: this CTA's units.  Where items are split, every CTA counts all items' tiles, an item's start as
-// kStart more, and takes an equal share of them.  (Parts of equal size for each row instead took 144 us for 32 rows
+// kStart (kStartRanges) more, and takes an equal share of them.  (Parts of equal size for each row instead took 144 us for 32 rows
 // of up to 16384 8-bit positions of 512, whose lengths differ; shares take 119.)
 template <int M, bool RANGES>
 __device__ __forceinline__ void find_units(const Kargs &k, Misc *m, int t, int threads)
@@ -395,7 +401,7 @@ __device__ __forceinline__ void find_units(const Kargs &k, Misc *m, int t, int t
             if (RANGES && e > 0) least = min(least, e);
         }
         if (RANGES && k.a.seen.window > 0 && most > 0) most -= numbers_of<RANGES>(k, it, least).skip;
-        m->before[i + 1] = weight_of<M>(k, most);
+        m->before[i + 1] = weight_of<M, RANGES>(k, most);
     }
     if (t == 0) m->before[0] = 0;
     __syncthreads();
@@ -512,11 +518,11 @@ __device__ __forceinline__ void make_unit(const Kargs &k, const Misc *m, int u, 
         int lo = 0, hi = static_cast<int>(tiles), slot = -1;
         if (k.p.split) {
             const bool one = k.p.items == 1;
-            const int at = one ? 0 : m->before[number], after = one ? weight_of<M>(k, most) : m->before[number + 1];
+            const int at = one ? 0 : m->before[number], after = one ? weight_of<M, RANGES>(k, most) : m->before[number + 1];
             const int all = one ? after : m->before[k.p.items];
             const Share s = share_of(all, k);
-            lo = max(s.from - at - kStart, 0);
-            hi = min(hi, max(min(s.to, after) - at - kStart, 0));
+            lo = max(s.from - at - start_of<RANGES>(k), 0);
+            hi = min(hi, max(min(s.to, after) - at - start_of<RANGES>(k), 0));
             slot = slot_of(s, u, at, after);
             if (one) note_parts(k, s, number, u, at, after, all);
         }

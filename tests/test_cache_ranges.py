@@ -95,6 +95,18 @@ def test_long_contexts_under_a_window(h, d):
                                 ends=torch.tensor(ends, dtype=torch.int32)) == 0
 
 
+# layouts as above; few rows over few tiles, some of them none
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
+@pytest.mark.parametrize("h,d,dv", [(7, 64, 64), (64, 128, 128), (100, 128, 96), (128, 192, 192), (33, 256, 256),
+                                    (64, 320, 200), (64, 512, 512)])
+def test_few_short_rows(h, d, dv, kind):
+    ps, mp, window, sinks = 16, 80, 600, 10
+    for b in (1, 2, 15, 16, 30, 60):
+        ends = torch.tensor([(1280, 0, 1, 611, 130, 128, 257, 1000)[i % 8] - i // 8 for i in range(b)], dtype=torch.int32)
+        assert check_window((b, 1, h, d, dv, ps, mp), kind, window, sinks, ends=ends) == 0
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("kind", ["bf16", "fp8"])
 def test_rows_outside_a_window_have_no_influence(kind):
@@ -151,11 +163,11 @@ def shared_tables(b, mp, common, pages, seed):
 
 
 def groups(rows, h, d, dv, b, mp, ps, shared):
-    """Whether a call attends to the prefix once for all: its parts need more scratch than a plain call's."""
+    """Whether a call attends to the prefix once for all: it has scratch, and other scratch than a plain call."""
     from gather_radix_select_gb300 import _native
     lib = _native.load()  # noqa: F811
-    return lib.sel_cache_attention_shared_workspace_size(rows, h, d, dv, b, mp, ps, shared) != \
-        lib.sel_cache_attention_workspace_size(rows, h, d, dv, b, mp, ps, 0, 0)
+    return lib.sel_cache_attention_shared_workspace_size(rows, h, d, dv, b, mp, ps, shared) not in \
+        (0, lib.sel_cache_attention_workspace_size(rows, h, d, dv, b, mp, ps, 0, 0))
 
 
 def check_shared(case, kind, shared, ends, seed=80, edit=None, grouped=None):
