@@ -216,7 +216,7 @@ def cache_attention(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tens
     ``window``: of the positions below its end a row sees the last ``window`` (1 or more) and the first ``sinks``.
     ``shared``: the first ``shared`` positions are the same cache rows for every sequence, usually because the page
     tables start with the same pages; they are then read and attended to once for the rows of all sequences where
-    that is less work (each may be read by way of any sequence's page table).  At most one of ``idx``, ``window`` and
+    that is less work (each may be read by way of the page table of any sequence that sees it).  At most one of ``idx``, ``window`` and
     ``shared`` is given.
 
     Returns ``(out, lse)``: bf16 [rows, h, dv], and fp32 [rows, h] (natural log of the sum of exponentials) with

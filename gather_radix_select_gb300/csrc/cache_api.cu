@@ -341,7 +341,7 @@ int sel_cache_append(const void *x, int x_dtype, int64_t tokens, int64_t x_strid
         (rotation->positions > 1 && rotation->stride % 4 != 0))
         return SEL_EALIGN;
     const int64_t runs = (d + SEL_CACHE_GROUP - 1) / SEL_CACHE_GROUP;
-    if (tokens > kIntMax / (16 * runs)) return SEL_EUNSUPPORTED;  // (16 lanes a run, 32-bit counts)
+    if (tokens > kIntMax / (16 * runs) || d >= int64_t{1} << 30) return SEL_EUNSUPPORTED;  // (16 lanes a run, 32-bit counts)
     if (q) {
         if (!aligned(q, 16) || !aligned(q_out, 16)) return SEL_EALIGN;
         const int64_t by_rows = product(tokens - 1, q_row_stride), by_heads = product(h - 1, q_head_stride);

@@ -468,8 +468,17 @@ __device__ __forceinline__ void make_unit(const Kargs &k, const Misc *m, int u, 
     }
     least = __reduce_min_sync(0xffffffffu, least);
     most = __reduce_max_sync(0xffffffffu, most);
+    uint32_t seq = it.seq;
     if (RANGES) {
         least_live = __reduce_min_sync(0xffffffffu, least_live);
+        if (it.prefix) {  // by the page table of a row that sees all that is to be looked up
+            seq = 0xffffffffu;
+#pragma unroll 1
+            for (int r = lane; r < rows; r += 32)
+                if (row_end_in<RANGES>(k, it, row0 + r) == most)
+                    seq = min(seq, static_cast<uint32_t>(row0 + r) / static_cast<uint32_t>(k.a.t.rows_per_seq));
+            seq = __reduce_min_sync(0xffffffffu, seq);
+        }
         const Numbers by = numbers_of<RANGES>(k, it, least_live);
         if (k.a.seen.window > 0 && most > 0 && by.skip > 0) {  // (a shared prefix's ends are numbers already)
             least = max(least - by.skip, 0);
@@ -510,7 +519,7 @@ __device__ __forceinline__ void make_unit(const Kargs &k, const Misc *m, int u, 
     if (lane == 0) {
         const int64_t tiles = (keys + M - 1) / M;
         w->row0 = row0;
-        w->seq = it.seq;
+        w->seq = seq;
         w->keys = keys;
         w->list_end = most;
         w->rows = rows;

@@ -46,13 +46,13 @@ typedef struct {
  *              rows of d on 16 bytes.
  *   q_out      bf16 [tokens, h, d] contiguous, on 16 bytes (unused without q).
  *              It may be q itself (bf16, contiguous): then only what is rotated
- *              is touched.  Else the two may not overlap.  A token whose position
- *              is negative or past the rotation's table has its queries copied
- *              as they are.
+ *              is touched.  Else the two may not overlap, nor may q_out overlap
+ *              another input or the cache.  A token whose position is negative
+ *              or past the rotation's table has its queries copied as they are.
  * Rows are rounded (SEL_BF16) or quantised (SEL_E4M3) as by sel_cache_write,
  * from the rotated fp32 values; queries are rounded to bf16 once.
- * SEL_EUNSUPPORTED: tokens * ceil(d / SEL_CACHE_GROUP) >= 2^27, h * d > 2^31 - 1
- * or tokens * h * d >= 2^40. */
+ * SEL_EUNSUPPORTED: tokens * ceil(d / SEL_CACHE_GROUP) >= 2^27, d >= 2^30, h * d
+ * > 2^31 - 1 or tokens * h * d >= 2^40. */
 SEL_API int sel_cache_append(const void *x, int x_dtype, int64_t tokens, int64_t x_stride, const sel_cache *cache,
                              const int32_t *page_table, int64_t b, int64_t max_pages, int64_t table_stride,
                              const void *positions, int pos_dtype, const sel_rotation *rotation, const void *q,
@@ -62,7 +62,9 @@ SEL_API int sel_cache_append(const void *x, int x_dtype, int64_t tokens, int64_t
 /* sel_cache_attention (idx == NULL) of rows that see, of the positions below
  * their end, the last `window` and those below `sinks`:
  *     p < end[r] and (p >= end[r] - window or p < sinks).
- * window >= 1, sinks >= 0. */
+ * window >= 1, sinks >= 0.  Pages that hold none of these positions are not
+ * looked up (a sequence's freed ones may be anything), but those that lie
+ * between the windows of a sequence's rows may be. */
 SEL_API int sel_cache_attention_window(const void *q, int64_t rows, int64_t h, int64_t q_row_stride,
                                        int64_t q_head_stride, const sel_cache *cache, const int32_t *page_table,
                                        int64_t b, int64_t max_pages, int64_t table_stride, const int32_t *end,
@@ -76,8 +78,9 @@ SEL_API size_t sel_cache_attention_window_workspace_size(int64_t rows, int64_t h
 
 /* sel_cache_attention (idx == NULL) where the first `shared` positions are the
  * same rows for all sequences, usually because their page tables start with the
- * same pages: each of these rows may be read by way of any sequence's page
- * table.  shared >= 0; more than the page table's positions means all of them. */
+ * same pages: each of these rows may be read by way of the page table of any
+ * sequence with a row that sees it.  shared >= 0; more than the page table's
+ * positions means all of them. */
 SEL_API int sel_cache_attention_shared(const void *q, int64_t rows, int64_t h, int64_t q_row_stride,
                                        int64_t q_head_stride, const sel_cache *cache, const int32_t *page_table,
                                        int64_t b, int64_t max_pages, int64_t table_stride, const int32_t *end,

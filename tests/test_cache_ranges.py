@@ -285,6 +285,21 @@ def test_rows_behind_the_prefix_are_their_sequences_own(kind):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
+def test_page_tables_of_padding_sequences_are_not_read(kind):
+    # sequences without a row that sees anything, the first of a tile's among them, whose page tables hold nothing; and
+    # one whose row ends within the prefix, with pages for no more than that
+    def lose(cache, table):
+        table[[0, 1, 16, 32, 39]] = -1
+        table[17, 10:] = -1
+
+    ends = torch.full((40,), 780, dtype=torch.int32) - torch.arange(40, dtype=torch.int32)
+    ends[[0, 1, 16, 32, 39]] = 0
+    ends[17] = 160
+    assert check_shared((40, 1, 8, 128, 128, 16, 50), kind, 704, ends, edit=lose, grouped=True) == 0
+
+
+@pytest.mark.gpu
 def test_a_page_outside_the_cache_in_the_prefix_is_reported():
     def lose(cache, table):
         table[:, 5] = 1 << 30
