@@ -259,6 +259,9 @@ __device__ __forceinline__ void copy_queries(const CacheAppendArgs &a, const Uni
     }
 }
 
+// The bytes bound what has queries: 8192 tokens of 512 with 16 heads' queries, bf16, 48.7 us in a graph, 5.8 TB/s; all in
+// one kind of unit, where every warp waited for some lane's angles, 110 us.  32 tokens with 64 heads' take 3 us: the
+// position, then the page and the angles, then the store.
 struct Blocks {
     uint32_t rows, turns;  // CTAs of the rows, of what is rotated of the queries; the rest copy
 };

@@ -41,6 +41,13 @@
 //   1024 rows x 64 heads over 512 selected 8-bit rows of 512   135 us   507 TFLOP/s (27%)
 //   32 rows x 64 heads over <= 16384 positions of 512, 8 bits  119 us   1840 GB/s, 448 TFLOP/s (27%)
 //   1 row over 1000 positions of 128                           10.9 us  (in a graph; latency: start, lookups, a tile, join)
+// With ranges (Seen): under a window, whose first and last tile of a unit are masked, and behind a prefix that all
+// sequences share, whose rows are then dealt out in tiles of their own (cache_attention.cu, plan_shared).
+//   1024 rows x 64 heads, window of 1024 + 4, rows of 512, bf16          217 us   635 TFLOP/s (33%)
+//   3 x 701 rows x 24 heads, window of 1000 + 7, rows of 192, bf16        66 us   493 TFLOP/s (26%)
+//   32 rows x 64 heads, window of 4096 + 16, 8-bit rows of 512            60 us   287 TFLOP/s, 1230 GB/s (18%)
+//   48 rows x 8 heads behind 204800 shared positions of 128, bf16         73 us   556 TFLOP/s (29%)
+//   64 rows x 16 heads behind 16384 shared positions of 512, 8 bits       86 us   412 TFLOP/s (21%)
 // Tried and slower: tiles of 64 positions (45 cycles an instruction of half the work); pairs of CTAs that share
 // a row (622 us against 385 then); TMA gathers of 4 rows (75 to 108 cycles for 512 bytes); bf16 rows through
 // registers (564 us); the next tile's rows prefetched into L2 (415 us: the copies fill the path already);
