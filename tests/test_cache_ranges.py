@@ -355,6 +355,49 @@ def test_captured_replayed_and_on_another_stream(form):
             assert torch.equal(out.view(torch.int16), want.view(torch.int16)) and torch.equal(lse, l64)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("scale", [0.03, -0.07, 0.0])
+@pytest.mark.parametrize("form", [{"window": 150, "sinks": 20}, {"shared": 640}], ids=["window", "shared"])
+def test_strided_queries_an_output_given_and_scales(form, scale):
+    import gather_radix_select_gb300 as sel
+    b, per, h, d, dv, ps, mp = 40, 2, 6, 144, 96, 16, 50
+    cache, scales = make_cache(40 + b * 10 + 2, ps, d, "fp8", 150)
+    table = shared_tables(b, mp + 3, 40, cache.shape[0] + 2000, 151) % cache.shape[0]
+    table = table[:, :mp]  # (rows of the page table are strided too)
+    fused = make_q(b * per, h + 3, d, 152)
+    q = fused[:, 2: 2 + h]
+    end = torch.tensor([mp * ps - 5 * i for i in range(b * per)], dtype=torch.int32)
+    out = torch.full((b * per, h, dv), 7.0, dtype=torch.bfloat16, device="cuda")
+    got, lse = sel.cache_attention(q, cache, table, scales=scales, end=end.cuda(), dv=dv, scale=scale, return_lse=True,
+                                   out=out, **form)
+    assert got is out
+    seen = seen_by_window(end, mp * ps, form["window"], form["sinks"]) if "window" in form else None
+    check_attention(out, lse, attend64(q, rows64(cache, scales), table, per, None if seen else end, seen, dv, scale))
+
+
+@pytest.mark.gpu
+def test_rows_past_2_to_the_32_elements():
+    # a cache of 8.6 GB: rows appended to its last pages and attended to there
+    import gather_radix_select_gb300 as sel
+    from tests.test_cache_append import rotation, turned
+    d, pages, n = 512, (1 << 23) + 40, 40
+    cache = torch.empty((pages, 1, d), dtype=torch.bfloat16, device="cuda")
+    last = torch.arange(pages - n, pages, dtype=torch.int32, device="cuda")
+    cache[last.long()] = 0
+    table = last[None]
+    angles = rotation(n, 64)
+    x = torch.randn((n, d), device="cuda")
+    sel.cache_append(x, cache, table, torch.arange(n, device="cuda"), torch.from_numpy(angles).cuda())
+    want = torch.from_numpy(turned(x.cpu().numpy(), range(n), angles, d - 64, False, "float32")).to(torch.bfloat16)
+    assert torch.equal(cache[last.long(), 0].cpu().view(torch.int16), want.view(torch.int16))
+    q = make_q(1, 16, d, 160)
+    out, lse = sel.cache_attention(q, cache, table, return_lse=True, window=30, sinks=3)
+    rows = want.double()[:, None]
+    here = torch.arange(n, dtype=torch.int32)[None]
+    seen = seen_by_window(torch.tensor([n]), n, 30, 3)
+    check_attention(out, lse, attend64(q, rows, here, 1, None, seen, d, 1 / math.sqrt(d)))
+
+
 @pytest.fixture
 def limit():
     from gather_radix_select_gb300 import _native
