@@ -564,6 +564,7 @@ __device__ __forceinline__ uint4 load16_if(const void *p, bool yes)
         : "l"(p), "r"(yes ? 1 : 0));
     return v;
 }
+__device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 __device__ __forceinline__ float load4_if(const float *p, bool yes, float other)
 {
     float v;
@@ -676,10 +677,14 @@ struct Loader {
         const uint32_t p = static_cast<uint32_t>(pos) + (RANGES && pos >= w->cut ? static_cast<uint32_t>(w->skip) : 0u), ps = static_cast<uint32_t>(k.a.c.page_size), col = p / ps;
         return Place{__ldg(k.a.t.table + w->seq * k.a.t.stride + col), static_cast<int>(p - col * ps)};
     }
+    __device__ __forceinline__ bool in_cache(Place at) const
+    {
+        return at.in_page != kNone && at.page >= 0 && at.page < k.a.c.pages;
+    }
     __device__ __forceinline__ Rows row_of(Place at) const
     {
         if (at.in_page == kNone) return Rows{-1, 0};
-        if (at.page < 0 || at.page >= k.a.c.pages) {
+        if (!in_cache(at)) {
             if (k.a.err_flag) atomicCAS(k.a.err_flag, 0, kCacheInval);
             return Rows{-1, 0};
         }
@@ -766,6 +771,10 @@ struct Loader {
         int64_t pos = position(ft + kNext);
         Place at = page_of(position(ft));
         int64_t mine = -1;  // row of the lane's line; -1: none
+        // Each line's next chunk that this warp will load is fetched into L2 while it works on this one: the second of a
+        // tile, and the first of the next one where no other CTA reads the same rows (32 rows over 16384 positions each, 8
+        // bits: 117 us without, 109 with the second, 106 with both; rows that are in L2 by others' doing lose 2% by the latter).
+        const bool far = !k.a.idx && !(RANGES && w->cut == 0x7fffffff);
         float sc[kScales];
         uint4 x[kLoads];
         auto fetch = [&]() {
@@ -784,6 +793,9 @@ struct Loader {
                 }
                 mine = cur.row;
                 fresh = false;
+                if (S > 1 && fc + S < C && lane < kPos && mine >= 0) prefetch_l2(data + mine + (fc + S) * 128);
+            } else if (S > 1 && far && lane < kPos && in_cache(at)) {
+                prefetch_l2(data + at.page * k.a.c.page_stride + at.in_page * k.a.c.row_stride + (fc + S - C) * 128);
             }
             const bool in = fc * 128 + vec * 16 < d;
 #pragma unroll
