@@ -36,21 +36,21 @@
 // before, the sums 5400).
 // Measured (GB300, device time; of the 1891 TFLOP/s and 6772 GB/s that plain products and copies reach):
 //   4096 rows x 64 heads over 512 selected rows of 512, bf16   371 us   649 TFLOP/s (34%)
-//   4 rows x 64 heads over 204800 positions of 512, bf16       169 us   4940 GB/s (73%)
+//   4 rows x 64 heads over 204800 positions of 512, bf16       165 us   5060 GB/s (75%)
 //   3 x 701 rows x 24 heads, 5000 positions of 192, causal     189 us   689 TFLOP/s (36%)
 //   1024 rows x 64 heads over 512 selected 8-bit rows of 512   135 us   507 TFLOP/s (27%)
-//   32 rows x 64 heads over <= 16384 positions of 512, 8 bits  119 us   1840 GB/s, 448 TFLOP/s (27%)
+//   32 rows x 64 heads over <= 16384 positions of 512, 8 bits  107 us   2050 GB/s, 498 TFLOP/s (30%)
 //   1 row over 1000 positions of 128                           10.9 us  (in a graph; latency: start, lookups, a tile, join)
 // With ranges (Seen): under a window, whose first and last tile of a unit are masked, and behind a prefix that all
 // sequences share, whose rows are then dealt out in tiles of their own (cache_attention.cu, plan_shared).
 //   1024 rows x 64 heads, window of 1024 + 4, rows of 512, bf16          217 us   635 TFLOP/s (33%)
 //   3 x 701 rows x 24 heads, window of 1000 + 7, rows of 192, bf16        66 us   493 TFLOP/s (26%)
-//   32 rows x 64 heads, window of 4096 + 16, 8-bit rows of 512            60 us   287 TFLOP/s, 1230 GB/s (18%)
+//   32 rows x 64 heads, window of 4096 + 16, 8-bit rows of 512            56 us   308 TFLOP/s, 1320 GB/s (19%)
 //   48 rows x 8 heads behind 204800 shared positions of 128, bf16         73 us   556 TFLOP/s (29%)
 //   64 rows x 16 heads behind 16384 shared positions of 512, 8 bits       86 us   412 TFLOP/s (21%)
 // Tried and slower: tiles of 64 positions (45 cycles an instruction of half the work); pairs of CTAs that share
 // a row (622 us against 385 then); TMA gathers of 4 rows (75 to 108 cycles for 512 bytes); bf16 rows through
-// registers (564 us); the next tile's rows prefetched into L2 (415 us: the copies fill the path already);
+// registers (564 us); the next tile's rows prefetched into L2 where other CTAs bring them there (415 us);
 // scores and values issued by a warp each (no change); a warp that looks up the rows for the others (448 us).
 // (A few per cent either way say little about an idea here: the order of the roles' code alone moves as much.)
 #pragma once
@@ -385,7 +385,7 @@ __device__ __forceinline__ int item_number(const Kargs &k, const Misc *m, int u)
 
 // All threads: this CTA's units.  Where items are split, every CTA counts all items' tiles, an item's start as
 // kStart (kStartRanges) more, and takes an equal share of them.  (Parts of equal size for each row instead took 144 us for 32 rows
-// of up to 16384 8-bit positions of 512, whose lengths differ; shares take 119.)
+// of up to 16384 8-bit positions of 512, whose lengths differ; shares took 119.)
 template <int M, bool RANGES>
 __device__ __forceinline__ void find_units(const Kargs &k, Misc *m, int t, int threads)
 {
@@ -692,6 +692,12 @@ struct Loader {
                     at.page * k.a.c.scale_page_stride + at.in_page * k.a.c.scale_row_stride};
     }
 
+    // Whether no other CTA reads the unit's rows, or only those of the same rows' other heads.
+    __device__ __forceinline__ bool alone() const
+    {
+        return !k.a.idx && !(RANGES && w->cut == 0x7fffffff) && w->rows == k.a.t.rows_per_seq;
+    }
+
     // This warp's validity bits of tile i of the unit.  (They have a barrier of their own: of the staged chunks only
     // the copies are waited for, which orders no ordinary store before them.)
     __device__ __forceinline__ void note(int i, const Rows &r) const
@@ -716,6 +722,7 @@ struct Loader {
         const int line0 = lw * kPos + (lane >> 4);
         const uint32_t to = smem_addr(smem) + (vec >> 3) * F::half_bytes + line0 * 128;
         const int halves = (d + 63) >> 6;
+        const bool far = alone();
         int64_t pos = position(1);
         Place at = page_of(position(0));
 #pragma unroll 1
@@ -743,6 +750,13 @@ struct Loader {
                 }
                 cp_async_arrive(&m->full[stage]);
                 at_ring.next(c);
+            }
+            // Where a tile fills the ring, the next one's rows wait for their places: into L2 meanwhile (16 rows over windows
+            // of 8192 positions of 512: 58.5 us without, 54.7 with; 320 elements, with a place to spare, 36.6 and 37.6).
+            if (F::ring == C && far && in_cache(at)) {
+                const uint16_t *next = data + at.page * k.a.c.page_stride + at.in_page * k.a.c.row_stride;
+#pragma unroll 1
+                for (int e = (lane >> 4) * 64; e < d; e += 128) prefetch_l2(next + e);
             }
         }
     }
@@ -774,7 +788,7 @@ struct Loader {
         // Each line's next chunk that this warp will load is fetched into L2 while it works on this one: the second of a
         // tile, and the first of the next one where no other CTA reads the same rows (32 rows over 16384 positions each, 8
         // bits: 117 us without, 109 with the second, 106 with both; rows that are in L2 by others' doing lose 2% by the latter).
-        const bool far = !k.a.idx && !(RANGES && w->cut == 0x7fffffff);
+        const bool far = alone();
         float sc[kScales];
         uint4 x[kLoads];
         auto fetch = [&]() {
