@@ -214,6 +214,7 @@ def cache_attention(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tens
     the kernel run out (about 2 s), ``err_flag`` gets SEL_ETIMEOUT and the rows lost by it are NaN.
 
     ``window``: of the positions below its end a row sees the last ``window`` (1 or more) and the first ``sinks``.
+    Pages that hold no position of any row may be gone: what the page table says of them has no influence.
     ``shared``: the first ``shared`` positions are the same cache rows for every sequence, usually because the page
     tables start with the same pages; they are then read and attended to once for the rows of all sequences where
     that is less work (each may be read by way of the page table of any sequence that sees it).  At most one of ``idx``, ``window`` and

@@ -193,6 +193,7 @@ struct Misc {
     uint64_t drained;        // every product is done
     uint32_t tmem;
     int abort;
+    int missing;             // (RANGES, window) a page was missing
     int units, item0;        // of this CTA: units, and, where tiles are shared out, the first one's item
     int before[kMaxItems + 1];  // tiles of the items before, where tiles are shared out
     alignas(16) float inv[kMaxCols];      // references, then 1 / sum
@@ -552,6 +553,38 @@ __device__ __forceinline__ void make_unit(const Kargs &k, const Misc *m, int u, 
     }
 }
 
+// One warp, under a window: a unit also holds what lies between its rows' windows, where pages may be gone, so that one was
+// missing is no finding yet.  The pages of the CTA's units that a row does see are looked up again.  (In the loop over
+// tiles or units this took registers: 3 x 701 rows of 192, 71 us in a graph instead of 65.)
+template <bool RANGES>
+__device__ __forceinline__ void report_missing(const Kargs &k, const Misc *m, int units, int lane)
+{
+    const int ps = static_cast<int>(k.a.c.page_size);  // (where a row has positions)
+#pragma unroll 1
+    for (int u = 0; u < units; ++u) {
+        const Item it = item_of<RANGES>(k, static_cast<uint32_t>(item_number<RANGES>(k, m, u)));
+        const int32_t *table = k.a.t.table + it.seq * k.a.t.stride;
+        int from = 0, to = 0;  // looked up for the row before
+#pragma unroll 1
+        for (int r = 0; r < it.rows; ++r) {
+            const int end = row_end(k, it.row0 + r), first = min(end, k.a.seen.sinks), last = max(end - k.a.seen.window, first);
+            const int at = last >= from && last <= to ? to : last;
+            from = last, to = end;
+            bool bad = false;
+#pragma unroll 1
+            for (int part = 0; part < 2; ++part) {
+                const int lo = part ? at : 0, hi = part ? end : first;
+#pragma unroll 1
+                for (int c = lo / ps + lane; lo < hi && c <= (hi - 1) / ps; c += 32) {
+                    const int page = __ldg(table + c);
+                    bad |= page < 0 || page >= k.a.c.pages;
+                }
+            }
+            if (bad) atomicCAS(k.a.err_flag, 0, kCacheInval);
+        }
+    }
+}
+
 // ------------------------------------------------------------------------------------ staging rows
 // Loads under a predicate, without a branch; 0 (or `other`) where it is false.
 __device__ __forceinline__ uint4 load16_if(const void *p, bool yes)
@@ -685,7 +718,10 @@ struct Loader {
     {
         if (at.in_page == kNone) return Rows{-1, 0};
         if (!in_cache(at)) {
-            if (k.a.err_flag) atomicCAS(k.a.err_flag, 0, kCacheInval);
+            if (RANGES && k.a.seen.window > 0)
+                m->missing = 1;  // (report_missing)
+            else if (k.a.err_flag)
+                atomicCAS(k.a.err_flag, 0, kCacheInval);
             return Rows{-1, 0};
         }
         return Rows{at.page * k.a.c.page_stride + at.in_page * k.a.c.row_stride,
@@ -1479,6 +1515,7 @@ __global__ void __launch_bounds__(Cfg<C, N, FP8>::threads, 1) attention_kernel(c
         mbar_init(&m->drained, 1);
         fence_mbar_init();
         m->abort = 0;
+        m->missing = 0;
     }
     if (warp == F::mma_warp) tmem_alloc(&m->tmem, 512);
     find_units<F::M, RANGES>(k, m, t, F::threads);
@@ -1515,6 +1552,9 @@ __global__ void __launch_bounds__(Cfg<C, N, FP8>::threads, 1) attention_kernel(c
             give(i);
         }
         cp_async_wait_all();
+        __syncwarp();  // (each warp sees what its lanes have noted)
+        if (RANGES && k.a.seen.window > 0 && k.a.err_flag && *const_cast<volatile int *>(&m->missing))
+            report_missing<RANGES>(k, m, units, lane);
     } else if (warp < F::soft_warps) {
         regs_to<F::soft_regs, (F::soft_regs > F::launch_regs)>();
         const int group = warp >> 2, quad = warp & 3;

@@ -62,9 +62,10 @@ SEL_API int sel_cache_append(const void *x, int x_dtype, int64_t tokens, int64_t
 /* sel_cache_attention (idx == NULL) of rows that see, of the positions below
  * their end, the last `window` and those below `sinks`:
  *     p < end[r] and (p >= end[r] - window or p < sinks).
- * window >= 1, sinks >= 0.  Pages that hold none of these positions are not
- * looked up (a sequence's freed ones may be anything), but those that lie
- * between the windows of a sequence's rows may be. */
+ * window >= 1, sinks >= 0.  The page table's entries for pages that hold no
+ * position of any of the sequence's rows may be anything (freed pages): they are
+ * no finding and have no influence.  (Those between the windows of rows whose
+ * ends lie apart may be looked up all the same.) */
 SEL_API int sel_cache_attention_window(const void *q, int64_t rows, int64_t h, int64_t q_row_stride,
                                        int64_t q_head_stride, const sel_cache *cache, const int32_t *page_table,
                                        int64_t b, int64_t max_pages, int64_t table_stride, const int32_t *end,
