@@ -91,10 +91,17 @@ def _index(idx, dev):
     return rows, n, stride if rows > 1 else n
 
 
+def _own(stream, dev):
+    """A stream of another device would run the kernels there, or leave the call unordered with what is on it."""
+    if stream.device != dev:
+        raise ValueError("stream must be one of the cache's device")
+
+
 def _launch(dev, stream, call):
     """``call(raw stream)`` with ``dev`` current and, where a stream is given, that stream current too (so that
     what the call allocates belongs to it)."""
     if stream is not None:
+        _own(stream, dev)
         with torch.cuda.device(dev), torch.cuda.stream(stream):
             return call(stream.cuda_stream)
     index = dev.index
@@ -162,6 +169,7 @@ def cache_append(x: torch.Tensor, cache: torch.Tensor, page_table: torch.Tensor,
     if stream is None:
         got = _native.binding().cache_append(*args)
     else:
+        _own(stream, cache.device)
         with torch.cuda.device(cache.device), torch.cuda.stream(stream):
             got = _native.binding().cache_append(*args)
     if got.__class__ is int:
@@ -234,6 +242,7 @@ def cache_attention(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tens
         if stream is None:
             got = _native.binding().cache_attention(*args)
         else:
+            _own(stream, cache.device)
             with torch.cuda.device(cache.device), torch.cuda.stream(stream):
                 got = _native.binding().cache_attention(*args)
         if got.__class__ is int:
