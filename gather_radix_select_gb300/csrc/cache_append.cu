@@ -170,6 +170,15 @@ __device__ __forceinline__ void store8(uint16_t *to, const float v[8])
     *reinterpret_cast<uint4 *>(to) = *reinterpret_cast<uint4 *>(o);
 }
 
+// Values that were bf16, as they were (a rounding would change the bits of some NaN).
+__device__ __forceinline__ void keep8(uint16_t *to, const float v[8])
+{
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = __byte_perm(__float_as_uint(v[2 * i]), __float_as_uint(v[2 * i + 1]), 0x7632);
+    *reinterpret_cast<uint4 *>(to) = make_uint4(o[0], o[1], o[2], o[3]);
+}
+
 // Units of the queries: `each` a head, `per_token` a token's.  Unit n of a CTA's, whose first one is unit `in_token` of
 // token `token0`: its token, head and place among the head's.
 struct Units {
@@ -199,7 +208,14 @@ __device__ __forceinline__ void turn_queries(const CacheAppendArgs &a, const Uni
     float u[8], v[8];
     load8(a.q, a.q_bf16 != 0, from, u);
     load8(a.q, a.q_bf16 != 0, from + second, v);
-    if (pos >= 0 && pos < a.rot_rows) {
+    uint16_t *to = a.q_out + (n.token * a.h + n.head) * a.c.d + e;
+    if (pos < 0 || pos >= a.rot_rows) {
+        if (a.q_bf16) {
+            keep8(to, u);
+            keep8(to + second, v);
+            return;
+        }
+    } else {
         const float *cos = a.rotation + pos * a.rot_stride + n.at * 8;
         float c[8], s[8];
         load8f(cos, c);
@@ -222,7 +238,6 @@ __device__ __forceinline__ void turn_queries(const CacheAppendArgs &a, const Uni
             }
         }
     }
-    uint16_t *to = a.q_out + (n.token * a.h + n.head) * a.c.d + e;
     store8(to, u);
     store8(to + second, v);
 }
