@@ -12,8 +12,8 @@ offsets, workspace slots, output positions, gathered key rows), skip the ones
 that would leave their buffer and report SEL_EBOUNDS in err_flag.  It is
 loaded instead of libsel.so when SEL_LIBRARY=debug is set.
 
-csrc/binding.cpp, the module _binding, is compiled by g++ against the installed PyTorch, whose version its file's name
-has (its ABI goes with the version).
+csrc/binding.cpp, the module _binding, is compiled by g++ against the installed PyTorch and the running Python, whose
+versions its folder's name has (its ABI goes with both).
 """
 from __future__ import annotations
 
@@ -94,7 +94,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
 
 def binding_path() -> str:
     import torch
-    return os.path.join(OUT_DIR, "binding-%s" % torch.__version__, "_binding.so")
+    return os.path.join(OUT_DIR, "binding-%s-%s" % (torch.__version__, sysconfig.get_config_var("SOABI")), "_binding.so")
 
 
 def build_binding(force: bool = False, verbose: bool = False) -> str:
