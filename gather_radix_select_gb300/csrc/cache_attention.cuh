@@ -728,10 +728,23 @@ struct Loader {
                     at.page * k.a.c.scale_page_stride + at.in_page * k.a.c.scale_row_stride};
     }
 
-    // Whether no other CTA reads the unit's rows, or only those of the same rows' other heads.
-    __device__ __forceinline__ bool alone() const
+    // The unit's tiles from this one on hold rows that no other CTA reads, or only those of the same rows' other heads: a
+    // neighbouring sequence has other pages there.  (Sequences share what they start with; 32 places are looked at.)  It
+    // decides what is fetched into L2 ahead, which costs where others bring the rows in: 64 rows x 64 heads whose page tables
+    // start with the same 16384 positions of 512 take 209 us with it and 193 without, 8 bits 226 and 224.  The look takes
+    // about 0.6 us a unit, so short units go without: 8-bit ones of 8 tiles took 55.9 us with it, 55.4 without.
+    __device__ __forceinline__ int alone_from() const
     {
-        return !k.a.idx && !(RANGES && w->cut == 0x7fffffff) && w->rows == k.a.t.rows_per_seq;
+        constexpr int kNever = 0x7fffffff;
+        if (k.a.idx || (RANGES && w->cut == kNever) || w->rows != k.a.t.rows_per_seq) return kNever;
+        const int64_t beside = (w->seq + 1) * k.a.t.rows_per_seq < k.a.rows ? w->seq + 1 : w->seq - 1;
+        if (beside < 0 || w->n < (FP8 ? 10 : 4)) return 0;
+        const int j = (w->lo + w->n * lane / 32) * F::M;
+        const uint32_t p = static_cast<uint32_t>(j) + (RANGES && j >= w->cut ? static_cast<uint32_t>(w->skip) : 0u);
+        const uint32_t col = p / static_cast<uint32_t>(k.a.c.page_size);
+        const bool same = __ldg(k.a.t.table + w->seq * k.a.t.stride + col) == __ldg(k.a.t.table + beside * k.a.t.stride + col);
+        const uint32_t other = ~__ballot_sync(0xffffffffu, same);
+        return other == 0 ? kNever : w->n * (__ffs(other) - 1) / 32;
     }
 
     // This warp's validity bits of tile i of the unit.  (They have a barrier of their own: of the staged chunks only
@@ -758,9 +771,9 @@ struct Loader {
         const int line0 = lw * kPos + (lane >> 4);
         const uint32_t to = smem_addr(smem) + (vec >> 3) * F::half_bytes + line0 * 128;
         const int halves = (d + 63) >> 6;
-        const bool far = alone();
         int64_t pos = position(1);
         Place at = page_of(position(0));
+        const int far = alone_from();  // (its lookups are under way with the first rows')
 #pragma unroll 1
         for (int it = 0; it < n; ++it) {
             const Rows cur = row_of(at);
@@ -789,7 +802,7 @@ struct Loader {
             }
             // Where a tile fills the ring, the next one's rows wait for their places: into L2 meanwhile (16 rows over windows
             // of 8192 positions of 512: 58.5 us without, 54.7 with; 320 elements, with a place to spare, 36.6 and 37.6).
-            if (F::ring == C && far && in_cache(at)) {
+            if (F::ring == C && it + 1 >= far && in_cache(at)) {
                 const uint16_t *next = data + at.page * k.a.c.page_stride + at.in_page * k.a.c.row_stride;
 #pragma unroll 1
                 for (int e = (lane >> 4) * 64; e < d; e += 128) prefetch_l2(next + e);
@@ -820,11 +833,11 @@ struct Loader {
         bool fresh = true;                              // rows of tile ft not looked up yet
         int64_t pos = position(ft + kNext);
         Place at = page_of(position(ft));
+        const int far = alone_from();  // (its lookups are under way with the first rows')
         int64_t mine = -1;  // row of the lane's line; -1: none
         // Each line's next chunk that this warp will load is fetched into L2 while it works on this one: the second of a
-        // tile, and the first of the next one where no other CTA reads the same rows (32 rows over 16384 positions each, 8
+        // tile, and the first of the next one where no other CTA reads the same rows (alone_from; 32 rows over 16384 positions each, 8
         // bits: 117 us without, 109 with the second, 106 with both; rows that are in L2 by others' doing lose 2% by the latter).
-        const bool far = alone();
         float sc[kScales];
         uint4 x[kLoads];
         auto fetch = [&]() {
@@ -844,7 +857,7 @@ struct Loader {
                 mine = cur.row;
                 fresh = false;
                 if (S > 1 && fc + S < C && lane < kPos && mine >= 0) prefetch_l2(data + mine + (fc + S) * 128);
-            } else if (S > 1 && far && lane < kPos && in_cache(at)) {
+            } else if (S > 1 && ft + 1 >= far && lane < kPos && in_cache(at)) {
                 prefetch_l2(data + at.page * k.a.c.page_stride + at.in_page * k.a.c.row_stride + (fc + S - C) * 128);
             }
             const bool in = fc * 128 + vec * 16 < d;
