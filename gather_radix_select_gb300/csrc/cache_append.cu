@@ -281,14 +281,23 @@ struct Blocks {
     uint32_t rows, turns;  // CTAs of the rows, of what is rotated of the queries; the rest copy
 };
 
-// Runs of a token that a group of lanes takes, where there are many, and CTAs an SM (64 registers, 48).  16384 rows of
-// 512, bf16 to 8 bits: 7.6 us; 12.7 a run at a time (the position, its page and what follows from them formed four
-// times), 8.7 with 48 registers, 9 by two runs.  From fp32, 4101 rows of 192 and 24 queries: 20.5 us, 21.3 with 64
-// registers.
+// Runs of a token that a group of lanes takes at most, where there are many, and CTAs an SM (64 registers, 48).  16384 rows
+// of 512, bf16 to 8 bits: 7.9 us; 13.0 a run at a time (the position, its page and what follows from them formed four
+// times), 9.3 by two runs.  From fp32, 4101 rows of 192 and 24 queries: 20.5 us, 21.3 with 64 registers.
 template <bool BF16>
 struct Shape {
     static constexpr int runs = BF16 ? 4 : 2, ctas = BF16 ? 4 : 5;
 };
+
+// Runs that a group of lanes takes of tokens of `runs` runs, where there are many: no more than a row has, since what is
+// held for the others costs registers all the same.  65536 rows from bf16 to 8 bits by 1, 2 and 4 runs: of 128 elements
+// 14.2, 14.2, 16.9 us, of 256 27.3, 17.3, 20.1, of 320 38.4, 31.7, 22.4, of 512 49.6, 34.2, 27.6; from fp32 by 1 and 2:
+// of 128 13.6, 15.4, of 256 25.5, 19.8, of 384 36.1, 35.8, of 512 45.2, 37.3.
+int deep_of(int64_t runs, bool bf16)
+{
+    const int most = bf16 ? Shape<true>::runs : Shape<false>::runs;
+    return runs == 1 ? 1 : runs == 2 ? 2 : most;
+}
 
 template <int R, bool BF16>
 __global__ void __launch_bounds__(kThreads, Shape<BF16>::ctas)
@@ -315,8 +324,9 @@ cudaError_t launch_cache_append(const CacheAppendArgs &a, cudaStream_t s)
 {
     const int64_t runs = (a.c.d + kCacheGroup - 1) / kCacheGroup;
     const int64_t sms = device_sm_count() > 0 ? device_sm_count() : 1, per_block = kThreads / kWriteLanes;
-    // few rows: a group of lanes for each run
-    const int64_t deep = a.tokens * runs > 4 * sms * per_block ? (a.x_bf16 ? Shape<true>::runs : Shape<false>::runs) : 1;
+    // few rows: a group of lanes for each run (rows of 512, bf16 to 8 bits, by one run and by four: 2432 rows 3.3 and 3.4 us,
+    // 3500 4.5 and 3.6)
+    const int64_t deep = a.tokens * runs > 4 * sms * per_block ? deep_of(runs, a.x_bf16 != 0) : 1;
     const int64_t groups = (runs + deep - 1) / deep, items = a.tokens * groups;
     const int64_t row_blocks = (items + per_block - 1) / per_block;
     // (rotated where they are, the queries' other elements stay)
@@ -327,8 +337,8 @@ cudaError_t launch_cache_append(const CacheAppendArgs &a, cudaStream_t s)
     const Blocks blocks{static_cast<uint32_t>(row_blocks), static_cast<uint32_t>(turn_blocks)};
     const Rows rows{static_cast<uint32_t>(items), divisor_of(static_cast<uint32_t>(groups)),
                     divisor_of(static_cast<uint32_t>(a.t.rows_per_seq)), shift_of(a.c.page_size)};
-    auto kernel = a.x_bf16 ? (deep > 1 ? cache_append_kernel<Shape<true>::runs, true> : cache_append_kernel<1, true>)
-                           : (deep > 1 ? cache_append_kernel<Shape<false>::runs, false> : cache_append_kernel<1, false>);
+    auto kernel = a.x_bf16 ? (deep == 4 ? cache_append_kernel<4, true> : deep == 2 ? cache_append_kernel<2, true> : cache_append_kernel<1, true>)
+                           : (deep == 2 ? cache_append_kernel<2, false> : cache_append_kernel<1, false>);
     kernel<<<static_cast<unsigned>(grid), kThreads, 0, s>>>(a, blocks, rows, turns, copies);
     return cudaGetLastError();
 }
