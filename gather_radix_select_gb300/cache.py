@@ -162,7 +162,8 @@ def cache_append(x: torch.Tensor, cache: torch.Tensor, page_table: torch.Tensor,
 
     With ``q`` [tokens, h, d] (bf16 or fp32, tokens and heads may be strided) the tokens' queries are rotated in the
     same launch and returned, bf16 [tokens, h, d] (``q_out``, which may be a contiguous bf16 ``q`` itself); those of a
-    padding token are returned as they are.  Without, None is returned.  A position past the page table or the
+    padding token are returned as they are.  Without, None is returned.  No input may overlap the cache's rows that are
+    written.  A position past the page table or the
     rotation's table, or on a page outside the cache, writes nothing and sets ``err_flag``.
     """
     args = (x, cache, page_table, positions, rotation, scales, first, interleaved, q, q_out, err_flag)

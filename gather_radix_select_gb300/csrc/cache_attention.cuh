@@ -45,9 +45,12 @@
 // sequences share, whose rows are then dealt out in tiles of their own (cache_attention.cu, plan_shared).
 //   1024 rows x 64 heads, window of 1024 + 4, rows of 512, bf16          217 us   635 TFLOP/s (33%)
 //   3 x 701 rows x 24 heads, window of 1000 + 7, rows of 192, bf16        66 us   493 TFLOP/s (26%)
-//   32 rows x 64 heads, window of 4096 + 16, 8-bit rows of 512            56 us   308 TFLOP/s, 1320 GB/s (19%)
+//   1024 rows x 64 heads, window of 1024 + 4, 8-bit rows of 512          253 us   546 TFLOP/s (28%)
+//   32 rows x 64 heads, window of 4096 + 16, 8-bit rows of 512            57 us   305 TFLOP/s, 1300 GB/s (19%)
+//   16 rows x 64 heads, window of 8192 + 4, bf16 rows of 512              54 us   2540 GB/s (37%)
 //   48 rows x 8 heads behind 204800 shared positions of 128, bf16         73 us   556 TFLOP/s (29%)
-//   64 rows x 16 heads behind 16384 shared positions of 512, 8 bits       86 us   412 TFLOP/s (21%)
+//   64 rows x 16 heads behind 16384 shared positions of 512, 8 bits       88 us   404 TFLOP/s (21%)
+//   64 rows x 64 heads whose page tables share 16384 positions, bf16     194 us   729 TFLOP/s (39%); 8 bits 224 us
 // Tried and slower: tiles of 64 positions (45 cycles an instruction of half the work); pairs of CTAs that share
 // a row (622 us against 385 then); TMA gathers of 4 rows (75 to 108 cycles for 512 bytes); bf16 rows through
 // registers (564 us); the next tile's rows prefetched into L2 where other CTAs bring them there (415 us);
@@ -107,7 +110,7 @@ constexpr int kMaxItems = 512;             // items whose tiles are shared out e
 constexpr int kMaxCtas = 512;              // CTAs that share at most
 constexpr int kStart = 1;                  // tiles that an item's start counts for there
 // With ranges, whose items are often short, what it does take (48 sequences behind 204800 positions of 128: the busiest
-// CTA 63 us with 1, the median 58; 77.9 us in all with 1, 76.8 with 2, 76.4 with 3, 77.4 with 4).
+// CTA 63 us with 1, the median 58; in all 1 to 4 are within 2% of one another, no more than a copy of the code differs by).
 constexpr int kStartRanges = 3;
 // A column's reference is set 2^kHeadroom above its largest weight so far and moves when a weight reaches
 // twice the reference.  bf16 has the range of fp32, so the small weights lose nothing by it down to 2^-102 of the
@@ -836,8 +839,8 @@ struct Loader {
         const int far = alone_from();  // (its lookups are under way with the first rows')
         int64_t mine = -1;  // row of the lane's line; -1: none
         // Each line's next chunk that this warp will load is fetched into L2 while it works on this one: the second of a
-        // tile, and the first of the next one where no other CTA reads the same rows (alone_from; 32 rows over 16384 positions each, 8
-        // bits: 117 us without, 109 with the second, 106 with both; rows that are in L2 by others' doing lose 2% by the latter).
+        // tile, and the first of the next one where no other CTA reads the same rows (alone_from; 32 rows over 16384 positions
+        // each, 8 bits: 117 us without, 109 with the second, 106 with both; asked for too, the second makes no difference).
         float sc[kScales];
         uint4 x[kLoads];
         auto fetch = [&]() {

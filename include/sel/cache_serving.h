@@ -3,7 +3,8 @@
  * does besides cache.h's operators.  New tokens' rows are appended at their
  * positions, rotated by them on the way; attention over a window of the
  * latest positions and a few first ones; attention of a batch whose sequences
- * share a long prefix, which is attended to once for all of them.
+ * share a long prefix, which is attended to once for all of them where their
+ * heads leave room in a tile and that makes less of the work.
  *
  * Conventions, cache format, page table and errors are cache.h's.
  */
@@ -33,6 +34,7 @@ typedef struct {
  * same tokens' queries.
  *   x          [tokens, x_stride] of x_dtype (SEL_F32 | SEL_BF16), d elements a
  *              token, rows on 16 bytes; token t belongs to sequence t / (tokens / b).
+ *              Neither it nor another input may overlap the rows that are written.
  *   page_table int32 [b, table_stride], max_pages columns used.
  *   positions  [tokens] of pos_dtype (SEL_I32 | SEL_I64): the row goes to row
  *              p % page_size of page page_table[s, p / page_size].  A negative
@@ -81,7 +83,10 @@ SEL_API size_t sel_cache_attention_window_workspace_size(int64_t rows, int64_t h
  * same rows for all sequences, usually because their page tables start with the
  * same pages: each of these rows may be read by way of the page table of any
  * sequence with a row that sees it.  shared >= 0; more than the page table's
- * positions means all of them. */
+ * positions means all of them.  It saves work where a tile of 64 (row, head)
+ * columns (128 where d <= 192) holds more rows than a sequence has: with more than
+ * 32 heads (64), or a sequence's rows filling it, each sequence attends to the
+ * prefix for itself. */
 SEL_API int sel_cache_attention_shared(const void *q, int64_t rows, int64_t h, int64_t q_row_stride,
                                        int64_t q_head_stride, const sel_cache *cache, const int32_t *page_table,
                                        int64_t b, int64_t max_pages, int64_t table_stride, const int32_t *end,
